@@ -22,6 +22,8 @@ MB_LIB_PATH = os.path.join(_HERE, "libbwta_microbench.so")
 
 BWTA_OK, BWTA_ERR_INVALID_ARG, BWTA_ERR_UNSUPPORTED, BWTA_ERR_ALIGNMENT, BWTA_ERR_CUDA = range(5)
 STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_DRAIN = 0x1, 0x2, 0x4
+STATUS_BAD_PAGE, STATUS_NO_PAGE = 0x8, 0x10
+KV_F16, KV_E4M3 = 0, 1
 TERNARY, BINARY = 0, 1
 ERROR_NAMES = {1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "ALIGNMENT", 4: "CUDA"}
 
@@ -29,6 +31,9 @@ EXPORTS = ["bwta_pack_weights", "bwta_quantize_pack_acts", "bwta_quantize_pack_a
            "bwta_gemm", "bwta_gemm_ex", "bwta_gemm_tc",
            "bwta_linear_decode", "bwta_attn_scores", "billm_pack_weights", "billm_gemm",
            "bwta_linear_decode_batched", "bwta_attn_softmax_ternarize", "bwta_attn_av",
+           "bwta_kv_append", "bwta_attn_decode_paged", "bwta_attn_prompt_paged",
+           "bwta_kv_reserve", "bwta_kv_free", "bwta_kv_fork", "bwta_kv_compact",
+           "bwta_kv_copy_pages",
            "bwta_selftest_gemm_timeout", "bwta_version"]
 GEMM_WEIGHTS_READY = 0x1
 
@@ -51,6 +56,18 @@ class DecodeJobC(C.Structure):
                 ("wbits", C.c_void_p), ("wscale", C.c_void_p), ("N", C.c_int64),
                 ("ldw_words", C.c_int64), ("group", C.c_int64), ("Y", C.c_void_p),
                 ("ldY", C.c_int64), ("dots", C.c_void_p), ("ldD", C.c_int64)]
+
+
+class KvCacheC(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("num_pages", C.c_int64), ("page_size", C.c_int64),
+                ("n_kv_heads", C.c_int64), ("head_dim", C.c_int64), ("page_stride", C.c_int64),
+                ("scale_stride", C.c_int64), ("type", C.c_int32)]
+
+
+class KvTableC(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("ld", C.c_int64), ("max_pages", C.c_int64),
+                ("n_slots", C.c_int64), ("kv_len", C.c_void_p), ("refcount", C.c_void_p)]
 
 
 _lib = None
@@ -87,6 +104,21 @@ def load_library(path: str = LIB_PATH):
                                                vp]
     lib.bwta_selftest_gemm_timeout.argtypes = [vp, vp, vp, i64, i64, vp, vp, i64, i64, i64, i64,
                                                vp, i64, vp, i64, i64, vp, vp]
+    kc, kt = C.POINTER(KvCacheC), C.POINTER(KvTableC)
+    lib.bwta_kv_append.argtypes = [kc, kt, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, vp]
+    lib.bwta_attn_decode_paged.argtypes = [kc, kt, vp, i64, vp, i64, i64, cf, i64, i64, vp, i64, vp,
+                                           i64, vp, vp]
+    lib.bwta_attn_prompt_paged.argtypes = [kc, kt, vp, i64, vp, i64, vp, i64, i64, cf, i64, i64, vp,
+                                           i64, vp, vp]
+    lib.bwta_kv_reserve.argtypes = [kt, i64, i64, vp, vp, i64, vp, vp]
+    lib.bwta_kv_free.argtypes = [kt, i64, i64, vp, i64, vp, vp]
+    lib.bwta_kv_fork.argtypes = [kc, i64, kt, vp, vp, i64, vp, i64, vp, vp]
+    lib.bwta_kv_compact.argtypes = [kc, i64, kt, vp, vp, i64, vp, vp]
+    lib.bwta_kv_copy_pages.argtypes = [kc, kc, i64, vp, vp, i64, vp, i64, vp, vp]
+    lib.bwta_attn_decode_workspace.argtypes = [i64, i64, i64]
+    lib.bwta_attn_decode_workspace.restype = i64
+    lib.bwta_kv_pages_workspace.argtypes = [i64, i64]
+    lib.bwta_kv_pages_workspace.restype = i64
     lib.bwta_version.restype = C.c_char_p
     for name in EXPORTS[:-1]:
         getattr(lib, name).restype = C.c_int
@@ -433,6 +465,305 @@ def billm_gemm(X: torch.Tensor, Wq: BillmWeights, status=None, out=None) -> torc
     _check("billm_gemm", lib.billm_gemm(_ptr(X), M, _row_stride(X), C.byref(cs), _ptr(Y),
                                         _row_stride(Y), _ptr(status), _stream()))
     return Y
+
+
+# ------------------------------------------------------------------ paged key-value cache
+class KvCache:
+    """One layer's pool of pages: k, v [num_pages, n_kv_heads, page_size, head_dim], fp16, or uint8
+    (E4M3 bytes) with fp32 scales [num_pages, n_kv_heads, page_size]. Pages may be further apart than
+    dense (a view of a larger buffer), the inner dimensions are dense. Keeps the tensors alive; their
+    storage must stay where it is."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "ref", "device")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        e4m3 = k.dtype == torch.uint8
+        assert k.is_cuda and k.dtype in (torch.float16, torch.uint8) and v.dtype == k.dtype
+        assert k.dim() == 4 and v.shape == k.shape and v.device == k.device
+        assert e4m3 == (k_scale is not None) == (v_scale is not None)
+        P, H, ps, D = k.shape
+
+        def stride(t, inner):
+            """Distance of pages; the dimensions inside a page must be dense."""
+            step = 1
+            for size, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+                assert size == 1 or st == step, "the dimensions inside a page must be dense"
+                step *= size
+            return t.stride(0) if t.shape[0] > 1 else inner
+
+        rows = H * ps
+        ld, ls = stride(k, rows * D), 0
+        assert stride(v, rows * D) == ld
+        if e4m3:
+            for t in (k_scale, v_scale):
+                assert t.dtype == torch.float32 and t.shape == k.shape[:3] and t.device == k.device
+            ls = stride(k_scale, rows)
+            assert stride(v_scale, rows) == ls
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.c = KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                          v_scale.data_ptr() if e4m3 else None, P, ps, H, D, ld, ls,
+                          KV_E4M3 if e4m3 else KV_F16)
+        self.ref = C.byref(self.c)
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, e4m3: bool = False,
+              device="cuda"):
+        shape = (num_pages, n_kv_heads, page_size, head_dim)
+        kv = [torch.empty(shape, dtype=torch.uint8 if e4m3 else torch.float16, device=device)
+              for _ in range(2)]
+        sc = [torch.empty(shape[:3], dtype=torch.float32, device=device) if e4m3 else None
+              for _ in range(2)]
+        return KvCache(kv[0], kv[1], sc[0], sc[1])
+
+
+class KvTable:
+    """Which pages hold which sequence: pages int32 [n_slots, max_pages], kv_len int32 [n_slots],
+    refcount int32 [num_pages] (needed by the page calls only). Keeps the tensors alive."""
+    __slots__ = ("pages", "kv_len", "refcount", "c", "ref", "device")
+
+    def __init__(self, pages, kv_len, refcount=None):
+        assert pages.is_cuda and pages.dtype == torch.int32 and pages.dim() == 2
+        assert pages.shape[1] <= 1 or pages.stride(1) == 1
+        assert kv_len.dtype == torch.int32 and kv_len.shape == pages.shape[:1]
+        assert kv_len.is_contiguous() and kv_len.device == pages.device
+        if refcount is not None:
+            assert refcount.dtype == torch.int32 and refcount.dim() == 1
+            assert refcount.is_contiguous() and refcount.device == pages.device
+        self.pages, self.kv_len, self.refcount, self.device = pages, kv_len, refcount, pages.device
+        n, m = pages.shape
+        self.c = KvTableC(pages.data_ptr(), max(pages.stride(0), m) if n > 1 else m, m, n,
+                          kv_len.data_ptr(), refcount.data_ptr() if refcount is not None else None)
+        assert n <= 1 or pages.stride(0) >= m
+        self.ref = C.byref(self.c)
+
+    @staticmethod
+    def empty(n_slots: int, max_pages: int, num_pages: int, device="cuda"):
+        """A table without sequences over a pool of free pages."""
+        return KvTable(torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device),
+                       torch.zeros(n_slots, dtype=torch.int32, device=device),
+                       torch.zeros(num_pages, dtype=torch.int32, device=device))
+
+
+class KvLayers:
+    """The layers of a page call (KvCache each, one geometry) as C descriptors, built once."""
+    __slots__ = ("caches", "c", "n", "num_pages", "page_size", "device")
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        assert self.caches and all(x.device == self.caches[0].device for x in self.caches)
+        self.c = (KvCacheC * len(self.caches))(*[x.c for x in self.caches])
+        self.n = len(self.caches)
+        self.num_pages, _, self.page_size, _ = self.caches[0].k.shape
+        self.device = self.caches[0].device
+
+
+def kv_layers(caches) -> KvLayers:
+    """Descriptors for the page calls, from a KvCache or a list of them."""
+    if isinstance(caches, KvLayers):
+        return caches
+    return KvLayers([caches] if isinstance(caches, KvCache) else caches)
+
+
+class _on:
+    """Makes a device the current one for a call, where it is not already."""
+    __slots__ = ("dev", "was")
+
+    def __init__(self, device):
+        self.dev = device.index
+        self.was = torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.was != self.dev:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.was != self.dev:
+            torch.cuda.set_device(self.was)
+
+
+def _ints(t, device):
+    """Pointer of a dense int32 vector on `device` (or None)."""
+    if t is None:
+        return None
+    assert t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.device == device
+    return t.data_ptr()
+
+
+def _status(t, device):
+    if t is None:
+        return None
+    assert t.dtype == torch.int32 and t.numel() >= 1 and t.device == device
+    return t.data_ptr()
+
+
+def _kv_rows(t, width, device):
+    """(pointer, row stride, rows) of rows of `width` values: [n, width] or [n, heads, dim]."""
+    assert t.device == device and t.dim() in (2, 3)
+    if t.dim() == 3:
+        assert t.shape[2] <= 1 or t.stride(2) == 1
+        assert t.shape[1] <= 1 or t.stride(1) == t.shape[2]
+        assert t.shape[1] * t.shape[2] == width
+    else:
+        assert t.shape[1] == width and (width <= 1 or t.stride(1) == 1)
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else width), t.shape[0]
+
+
+def bwta_kv_append(cache: KvCache, table: KvTable, k, v, slots=None, cu_q=None, status=None):
+    """New tokens' keys and values, fp32 or fp16 [rows, n_kv_heads * head_dim] (or three dimensions),
+    into the pages. Without cu_q one row for each slot (or for each of `slots`); with it rows
+    cu_q[s] .. cu_q[s+1] belong to sequence s and end at its kv_len."""
+    lib = _L()
+    dev = cache.device
+    assert table.device == dev and k.dtype == v.dtype and k.dtype in (torch.float16, torch.float32)
+    width = cache.c.n_kv_heads * cache.c.head_dim
+    kp, ldk, n = _kv_rows(k, width, dev)
+    vp, ldv, nv = _kv_rows(v, width, dev)
+    assert n == nv
+    n_seq = _n_seq(table, slots, cu_q, n)
+    with _on(dev):
+        rc = lib.bwta_kv_append(cache.ref, table.ref, _ints(slots, dev), n_seq, _ints(cu_q, dev), n,
+                                kp, ldk, vp, ldv, int(k.dtype == torch.float32),
+                                _status(status, dev), _stream())
+    _check("bwta_kv_append", rc)
+
+
+def _n_seq(table, slots, cu_q, rows):
+    n = slots.shape[0] if slots is not None else (cu_q.shape[0] - 1 if cu_q is not None else rows)
+    assert cu_q is None or cu_q.shape[0] == n + 1
+    assert cu_q is not None or rows == n
+    return n
+
+
+def bwta_attn_decode_paged(q, cache: KvCache, table: KvTable, softmax_scale: float, window: int = 0,
+                           sinks: int = 0, slots=None, workspace=None, status=None, out=None):
+    """Attention of one new token of each sequence over its pages. q fp16 [n_seq, n_heads, head_dim]
+    -> out, the same shape. workspace: uint8 of decode_workspace() bytes (allocated when not given)."""
+    lib = _L()
+    dev, D = cache.device, cache.c.head_dim
+    assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
+    n, heads = q.shape[0], q.shape[1]
+    qp, ldq, _ = _kv_rows(q, heads * D, dev)
+    n_seq = _n_seq(table, slots, None, n)
+    if out is None:
+        out = torch.empty((n, heads, D), dtype=torch.float16, device=dev)
+    assert out.dtype == torch.float16 and out.shape == q.shape
+    op, ldo, _ = _kv_rows(out, heads * D, dev)
+    if workspace is None:
+        workspace = decode_workspace(heads, cache)
+    assert workspace.device == dev and workspace.is_contiguous()
+    with _on(dev):
+        rc = lib.bwta_attn_decode_paged(cache.ref, table.ref, _ints(slots, dev), n_seq, qp, ldq,
+                                        heads, softmax_scale, window, sinks, op, ldo,
+                                        workspace.data_ptr(), workspace.nbytes,
+                                        _status(status, dev), _stream())
+    _check("bwta_attn_decode_paged", rc)
+    return out
+
+
+def decode_workspace(n_heads: int, cache: KvCache):
+    """A workspace for bwta_attn_decode_paged; calls that may overlap in time need one each."""
+    c = cache.c
+    n = load_library().bwta_attn_decode_workspace(n_heads, c.n_kv_heads, c.head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def bwta_attn_prompt_paged(q, cu_q, cache: KvCache, table: KvTable, softmax_scale: float,
+                           window: int = 0, sinks: int = 0, slots=None, status=None, out=None):
+    """Attention of many new tokens of each sequence over its pages, which hold them already.
+    q fp16 [rows, n_heads, head_dim], rows cu_q[s] .. cu_q[s+1] the newest of sequence s -> out, the
+    same shape (rows past the last sequence are left as they are)."""
+    lib = _L()
+    dev, D = cache.device, cache.c.head_dim
+    assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
+    n, heads = q.shape[0], q.shape[1]
+    qp, ldq, _ = _kv_rows(q, heads * D, dev)
+    n_seq = _n_seq(table, slots, cu_q, n)
+    if out is None:
+        out = torch.empty((n, heads, D), dtype=torch.float16, device=dev)
+    assert out.dtype == torch.float16 and out.shape == q.shape
+    op, ldo, _ = _kv_rows(out, heads * D, dev)
+    with _on(dev):
+        rc = lib.bwta_attn_prompt_paged(cache.ref, table.ref, _ints(slots, dev), n_seq,
+                                        _ints(cu_q, dev), n, qp, ldq, heads, softmax_scale, window,
+                                        sinks, op, ldo, _status(status, dev), _stream())
+    _check("bwta_attn_prompt_paged", rc)
+    return out
+
+
+def bwta_kv_reserve(table: KvTable, page_size: int, slots, n_new, status=None):
+    """Room for n_new[i] more tokens in slot slots[i]; raises kv_len."""
+    lib = _L()
+    dev = table.device
+    assert table.refcount is not None and slots.shape == n_new.shape
+    with _on(dev):
+        rc = lib.bwta_kv_reserve(table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
+                                 _ints(n_new, dev), slots.shape[0], _status(status, dev), _stream())
+    _check("bwta_kv_reserve", rc)
+
+
+def bwta_kv_free(table: KvTable, page_size: int, slots, status=None):
+    """Give up the slots' pages."""
+    lib = _L()
+    dev = table.device
+    assert table.refcount is not None
+    with _on(dev):
+        rc = lib.bwta_kv_free(table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
+                              slots.shape[0], _status(status, dev), _stream())
+    _check("bwta_kv_free", rc)
+
+
+def pages_workspace(num_pages: int, n: int, device="cuda"):
+    """A workspace for the page calls: num_pages of the pool (fork, compact) and n list entries."""
+    return torch.empty(load_library().bwta_kv_pages_workspace(num_pages, n), dtype=torch.uint8,
+                       device=device)
+
+
+def bwta_kv_fork(caches, table: KvTable, src, dst, workspace=None, status=None):
+    """Make slot dst[i] a copy of slot src[i], in all layers: full pages shared, the rest copied."""
+    lib = _L()
+    l = kv_layers(caches)
+    dev = l.device
+    assert table.refcount is not None and table.refcount.shape[0] == l.num_pages
+    assert src.shape == dst.shape and table.device == dev
+    ws = pages_workspace(l.num_pages, src.shape[0], dev) if workspace is None else workspace
+    assert ws.device == dev and ws.is_contiguous()
+    with _on(dev):
+        rc = lib.bwta_kv_fork(l.c, l.n, table.ref, _ints(src, dev), _ints(dst, dev), src.shape[0],
+                              ws.data_ptr(), ws.nbytes, _status(status, dev), _stream())
+    _check("bwta_kv_fork", rc)
+
+
+def bwta_kv_compact(caches, table: KvTable, workspace=None, status=None, out=None):
+    """Move the pages in use to the front of the pool, in all layers. Returns int32 [1]: how many."""
+    lib = _L()
+    l = kv_layers(caches)
+    dev = l.device
+    assert table.refcount is not None and table.refcount.shape[0] == l.num_pages
+    assert table.device == dev
+    ws = pages_workspace(l.num_pages, 0, dev) if workspace is None else workspace
+    assert ws.device == dev and ws.is_contiguous()
+    if out is None:
+        out = torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(dev):
+        rc = lib.bwta_kv_compact(l.c, l.n, table.ref, _ints(out, dev), ws.data_ptr(), ws.nbytes,
+                                 _status(status, dev), _stream())
+    _check("bwta_kv_compact", rc)
+    return out
+
+
+def bwta_kv_copy_pages(src_caches, dst_caches, src_pages, dst_pages, workspace=None, status=None):
+    """Copy page src_pages[i] of src to page dst_pages[i] of dst, in all layers."""
+    lib = _L()
+    a, b = kv_layers(src_caches), kv_layers(dst_caches)
+    dev = a.device
+    assert b.device == dev and a.n == b.n and src_pages.shape == dst_pages.shape
+    n = src_pages.shape[0]
+    ws = pages_workspace(0, n, dev) if workspace is None else workspace
+    assert ws.device == dev and ws.is_contiguous()
+    with _on(dev):
+        rc = lib.bwta_kv_copy_pages(a.c, b.c, a.n, _ints(src_pages, dev), _ints(dst_pages, dev), n,
+                                    ws.data_ptr(), ws.nbytes, _status(status, dev), _stream())
+    _check("bwta_kv_copy_pages", rc)
 
 
 # ------------------------------------------------------------------ helpers

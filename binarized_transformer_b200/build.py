@@ -26,9 +26,9 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcomp
                 "-I", os.path.join(ROOT, "include")]
 
 LIB_SOURCES = ["pack.cu", "gemm.cu", "decode.cu", "gemm_tc.cu", "attn.cu", "billm.cu", "billm_tc.cu",
-               "abi.cu"]
+               "kv_append.cu", "kv_pages.cu", "attn_paged.cu", "kv_abi.cu", "abi.cu"]
 MB_SOURCES = ["microbench.cu"]
-HEADERS = ["common.cuh", "tma.cuh", "quant.cuh", "tcgen05.cuh"]
+HEADERS = ["common.cuh", "tma.cuh", "quant.cuh", "tcgen05.cuh", "kv.cuh"]
 
 
 def _mtime(p):

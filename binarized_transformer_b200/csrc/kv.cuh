@@ -1,0 +1,126 @@
+// kv.cuh -- views of the paged key-value cache and its table for the kernels,
+// and the launchers of the calls on them (validated in kv_abi.cu).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace bwta {
+
+constexpr int KV_MAX_D = 128;
+
+// One layer's pool. Strides in elements of k / v and in floats of the scales.
+struct KvView {
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  int64_t page_stride, scale_stride;
+  int32_t num_pages, ps, H, D;
+};
+
+struct KvRows {
+  const int32_t *pages;
+  const int32_t *len;
+  const int32_t *slots;  // NULL: sequence s is slot s
+  int64_t ld;
+  int32_t max_pages, n_slots;
+};
+
+// Slot of sequence s, or -1 when it is outside the table.
+__device__ __forceinline__ int32_t kv_slot(const KvRows &r, int64_t s) {
+  if (!r.slots) return (int32_t)s;
+  const int32_t v = r.slots[s];
+  return (uint32_t)v < (uint32_t)r.n_slots ? v : -1;
+}
+
+// Tokens of a slot, cut to its row of pages; sets bad when it had to cut.
+__device__ __forceinline__ int32_t kv_length(const KvRows &r, int32_t slot, int32_t ps, bool &bad) {
+  if (slot < 0) {
+    bad = true;
+    return 0;
+  }
+  const int32_t len = r.len[slot];
+  const int64_t room = (int64_t)r.max_pages * ps;
+  if (len < 0 || len > room) {
+    bad = true;
+    return len < 0 ? 0 : (int32_t)room;
+  }
+  return len;
+}
+
+// The sequence whose rows [cu[s], cu[s+1]) hold row t, for cu[0] <= t < cu[n].
+__device__ __forceinline__ int64_t kv_find_seq(const int32_t *cu, int64_t n, int64_t t) {
+  int64_t lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct AttnArgs {
+  KvView c;
+  KvRows r;
+  const int32_t *cu_q;  // NULL: one row each
+  int64_t n_seq, total_q;
+  const uint16_t *q;
+  int64_t ldq;
+  int32_t n_heads;
+  float scale;
+  int64_t window, sinks;
+  uint16_t *out;
+  int64_t ldo;
+  int32_t *d_status;
+};
+
+struct KvAppendArgs {
+  KvView c;
+  KvRows r;
+  const int32_t *cu_q;
+  int64_t n_seq, total_q;
+  const void *k, *v;
+  int64_t ldk, ldv;
+  bool f32, e4m3;
+  int32_t *d_status;
+};
+
+// One layer's buffers in a page call.
+struct KvLayer {
+  uint8_t *k, *v;
+  float *ks, *vs;
+};
+struct KvLayers {
+  KvLayer src[BWTA_KV_MAX_LAYERS];
+  KvLayer dst[BWTA_KV_MAX_LAYERS];
+};
+struct KvGeometry {
+  int64_t kv_bytes;         // of one page of k (or v)
+  int64_t src_kv_stride, dst_kv_stride;  // bytes between pages
+  int64_t sc_bytes, src_sc_stride, dst_sc_stride;  // the same for the scales; 0: none
+  int32_t n_layers, src_pages, dst_pages, page_size;
+};
+struct KvTableView {
+  int32_t *pages, *len, *ref;
+  int64_t ld;
+  int32_t max_pages, n_slots;
+};
+
+int64_t kv_pages_ws_ints(int64_t num_pages, int64_t n);
+cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
+cudaError_t launch_attn_simple(const AttnArgs &a, bool e4m3, cudaStream_t s);
+cudaError_t launch_kv_reserve(const KvTableView &t, int32_t num_pages, int32_t ps,
+                              const int32_t *slots, const int32_t *n_new, int32_t n,
+                              int32_t *d_status, cudaStream_t s);
+cudaError_t launch_kv_free(const KvTableView &t, int32_t num_pages, int32_t ps,
+                           const int32_t *slots, int64_t n, int32_t *d_status, cudaStream_t s);
+cudaError_t launch_kv_fork(const KvLayers &l, const KvGeometry &g, const KvTableView &t,
+                           const int32_t *src, const int32_t *dst, int32_t n, int32_t *ws,
+                           int32_t *d_status, cudaStream_t s);
+cudaError_t launch_kv_compact(const KvLayers &l, const KvGeometry &g, const KvTableView &t,
+                              int32_t *n_used, int32_t *ws, int32_t *d_status, cudaStream_t s);
+cudaError_t launch_kv_copy(const KvLayers &l, const KvGeometry &g, bool same, const int32_t *src,
+                           const int32_t *dst, int64_t n, int32_t *ws, int32_t *d_status,
+                           cudaStream_t s);
+
+}  // namespace bwta

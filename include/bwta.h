@@ -345,6 +345,189 @@ int billm_pack_weights(const float *W, int64_t ldW, int split, const billm_weigh
 int billm_gemm(const uint16_t *X, int64_t M, int64_t ldX, const billm_weights *W, float *Y,
                int64_t ldY, int32_t *d_status, bwta_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The paged key-value cache and the attention that reads it: what stands
+ * between a layer's q/k/v projections and its output projection when tokens
+ * come one at a time. One layer's pool holds num_pages pages of page_size
+ * tokens; a table, shared by all layers, says which pages hold which sequence
+ * (a "slot"), how long it is and how many slots share each page.
+ *
+ * Life of a step: bwta_kv_reserve makes room for the new tokens and raises
+ * kv_len; then for every layer bwta_kv_append writes their keys and values and
+ * bwta_attn_decode_paged / bwta_attn_prompt_paged attends. The page calls work
+ * on the table and on all layers at once. Nothing is read back to the host, so
+ * a step can be captured into a graph.
+ *
+ * A table, list or length that does not make sense never leads a kernel out of
+ * its buffers: BWTA_STATUS_BAD_PAGE is OR-ed into *d_status and what the call
+ * says about such an entry happens. */
+#define BWTA_STATUS_BAD_PAGE 0x8  /* a page, slot, length or list entry out of range or listed twice */
+#define BWTA_STATUS_NO_PAGE 0x10  /* not enough free pages: the requests that did not fit were not made */
+
+#define BWTA_KV_F16 0  /* fp16 values */
+#define BWTA_KV_E4M3 1 /* E4M3 bytes, value = byte * scale of its token and head (a power of two) */
+#define BWTA_ROWS_F16 0
+#define BWTA_ROWS_F32 1
+
+#define BWTA_KV_MAX_LAYERS 128  /* layers of one page call */
+#define BWTA_KV_MAX_LIST 2048   /* slots in one list of a page call */
+#define BWTA_KV_MAX_POOL (1 << 19) /* pages of a pool that the page calls take */
+
+/* One layer's pool (device buffers; the struct itself is read during the call).
+ *  k, v      [num_pages][n_kv_heads][page_size][head_dim], fp16 or E4M3, inner
+ *            three dimensions dense, pages page_stride elements apart
+ *  k_scale, v_scale   E4M3: fp32 [num_pages][n_kv_heads][page_size], pages
+ *            scale_stride floats apart; NULL for fp16
+ * head_dim a multiple of 8, 8 .. 128; page_size a multiple of 16, 16 .. 65536;
+ * strides of pages multiples of 16 bytes; buffers 16-byte aligned.
+ * An E4M3 row (one token, one head) has the scale 2^e with the smallest e in
+ * -15 .. 8 for which max|x| <= 448 * 2^e (e = 0 for a row of zeros), and holds
+ * x * 2^-e rounded to the nearest E4M3 value, ties to even, limited to +-448
+ * (+-240 for e = 8). Scaling by a power of two is exact, so each value is
+ * rounded once, and every value that the cache can hold is also an fp16 value. */
+typedef struct bwta_kv_cache {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t num_pages, page_size, n_kv_heads, head_dim, page_stride, scale_stride;
+  int32_t type; /* BWTA_KV_F16 or BWTA_KV_E4M3 */
+} bwta_kv_cache;
+
+/* Which pages hold which sequence. A slot of length len owns the first
+ * ceil(len / page_size) entries of its row; the calls below write -1 to the
+ * entries that they give up.
+ *  pages     int32 [n_slots][ld], the first max_pages entries of a row are used
+ *  kv_len    int32 [n_slots] tokens of each slot (0 = empty)
+ *  refcount  int32 [num_pages] slots that hold each page (0 = free); the append
+ *            and attention calls do not read it (may be NULL there) */
+typedef struct bwta_kv_table {
+  int32_t *pages;
+  int64_t ld, max_pages, n_slots;
+  int32_t *kv_len;
+  int32_t *refcount;
+} bwta_kv_table;
+
+/* Write new tokens' keys and values into the pages.
+ *  slots    int32 [n_seq] the slot of each sequence, NULL = slots 0 .. n_seq-1
+ *  cu_q     int32 [n_seq+1] ascending, first 0: rows cu_q[s] .. cu_q[s+1]-1 are
+ *           sequence s's newest tokens, i.e. row i of n goes to position
+ *           kv_len - n + i (kv_len counts them already). NULL = one row each
+ *           (total_q must be n_seq). Rows at and past cu_q[n_seq] are not read.
+ *  k, v     rows of n_kv_heads * head_dim fp16 or fp32 values (row_type), ldk and
+ *           ldv elements apart; 16-byte aligned, strides multiples of 16 bytes
+ *  A token whose position is negative, past the row of pages or on a page
+ *  outside the pool is left out (BAD_PAGE). NONFINITE: a value that fp16 cannot
+ *  hold; an fp16 cache then holds what the conversion gives (Inf or NaN), the
+ *  bytes of that E4M3 row are unspecified.
+ *  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+int bwta_kv_append(const bwta_kv_cache *cache, const bwta_kv_table *table, const int32_t *slots,
+                   int64_t n_seq, const int32_t *cu_q, int64_t total_q, const void *k, int64_t ldk,
+                   const void *v, int64_t ldv, int row_type, int32_t *d_status,
+                   bwta_stream_t stream);
+
+/* Attention of one new token of each sequence over its pages. For query head h
+ * of sequence s, at position p = kv_len - 1, over its key head h / (n_heads /
+ * n_kv_heads):
+ *     o = sum_j w_j v_j / sum_j w_j,  w_j = exp(softmax_scale * q . k_j - max)
+ * over the visible keys: j <= p, and with window > 0 also j > p - window or
+ * j < sinks. An empty slot gives zeros. Scores, maxima, sums and the weighted
+ * sum are fp32; the weights are rounded to fp16 before they meet V (their sum
+ * takes them unrounded), and o is rounded to fp16 once.
+ *  q        fp16 [n_seq][n_heads * head_dim], rows ldq elements apart
+ *  out      fp16 [n_seq][n_heads * head_dim], rows ldo elements apart
+ *  window   0 = every key, else >= 1; sinks >= 0 (only with a window)
+ *  workspace, workspace_bytes   device memory (16-byte aligned) of at least
+ *           bwta_attn_decode_workspace() bytes; its contents need no
+ *           preparation and do not outlive the call. Calls that can run at the
+ *           same time need one each.
+ *  softmax_scale finite and > 0; n_heads a multiple of n_kv_heads; q and out
+ *  16-byte aligned, strides multiples of 8 elements.
+ *  BAD_PAGE: a page outside the pool, a slot outside the table (read as empty)
+ *  or a length past the row of pages (cut there); the outputs of that sequence
+ *  are unspecified. NONFINITE: an output is not finite, because a visible key
+ *  or value or the query was not. Keys that are not visible have no influence,
+ *  whatever they hold.
+ *  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+int bwta_attn_decode_paged(const bwta_kv_cache *cache, const bwta_kv_table *table,
+                           const int32_t *slots, int64_t n_seq, const uint16_t *q, int64_t ldq,
+                           int64_t n_heads, float softmax_scale, int64_t window, int64_t sinks,
+                           uint16_t *out, int64_t ldo, void *workspace, int64_t workspace_bytes,
+                           int32_t *d_status, bwta_stream_t stream);
+int64_t bwta_attn_decode_workspace(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
+
+/* The same attention for many new tokens of each sequence, whose keys and
+ * values are in the pages already: row i of sequence s's n rows is the query at
+ * position kv_len - n + i (a whole prompt when n = kv_len, a chunk of one
+ * otherwise). A row at a negative position sees nothing and gives zeros. Rows
+ * at and past cu_q[n_seq] are neither read nor written.
+ *  cu_q     int32 [n_seq+1] ascending, first 0, last <= total_q
+ *  q, out   fp16 [total_q][n_heads * head_dim]
+ *  Limits: n_heads / n_kv_heads <= 128.
+ *  The rest as bwta_attn_decode_paged, but a value that is visible to one row
+ *  of a sequence and not finite may reach the sequence's other rows. TIMEOUT
+ *  and DRAIN as for the other tensor-core calls. */
+int bwta_attn_prompt_paged(const bwta_kv_cache *cache, const bwta_kv_table *table,
+                           const int32_t *slots, int64_t n_seq, const int32_t *cu_q,
+                           int64_t total_q, const uint16_t *q, int64_t ldq, int64_t n_heads,
+                           float softmax_scale, int64_t window, int64_t sinks, uint16_t *out,
+                           int64_t ldo, int32_t *d_status, bwta_stream_t stream);
+
+/* Room for n_new[i] more tokens in slot slots[i]: the pages that its row lacks
+ * are the free pages of the lowest numbers, handed out in the order of the
+ * list; then kv_len grows. A request that the remaining free pages cannot meet
+ * is not made (its kv_len stays; NO_PAGE), nor is any later one that needs a
+ * page. Refused as BAD_PAGE, without effect: a slot out of range or listed
+ * before, a negative count, a row of pages that would be too short.
+ *  slots, n_new  device int32 [n], n <= BWTA_KV_MAX_LIST
+ *  num_pages     pages of the pool = length of refcount, <= BWTA_KV_MAX_POOL
+ *  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int bwta_kv_reserve(const bwta_kv_table *table, int64_t num_pages, int64_t page_size,
+                    const int32_t *slots, const int32_t *n_new, int64_t n, int32_t *d_status,
+                    bwta_stream_t stream);
+
+/* Give up slots: their pages' counts go down by one, their rows' entries become
+ * -1, kv_len 0. A slot listed twice is freed once. BAD_PAGE: a slot or page out
+ * of range, or a page whose count was 0 already (it stays 0). n any size. */
+int bwta_kv_free(const bwta_kv_table *table, int64_t num_pages, int64_t page_size,
+                 const int32_t *slots, int64_t n, int32_t *d_status, bwta_stream_t stream);
+
+/* Make slot dst[i] a copy of slot src[i] as it was before the call: full pages
+ * are shared (their counts go up), a last page that is not full is copied in
+ * every layer into the free page of the lowest number (in the order of the
+ * list), since both slots will write to it. One source may have many copies. A
+ * fork that finds no free page is not made (dst stays empty; NO_PAGE), nor is
+ * any later one that needs a page. Refused as BAD_PAGE, without effect: slots
+ * out of range, dst not empty or listed before, src with a length past its row.
+ * An entry of src's row outside the pool is passed on as it is (BAD_PAGE).
+ *  caches     host array of n_layers layers of one geometry (<= BWTA_KV_MAX_LAYERS)
+ *  src, dst   device int32 [n], n <= BWTA_KV_MAX_LIST
+ *  workspace  device, 16-byte aligned, bwta_kv_pages_workspace(num_pages, n) bytes;
+ *             as for bwta_attn_decode_paged */
+int bwta_kv_fork(const bwta_kv_cache *caches, int64_t n_layers, const bwta_kv_table *table,
+                 const int32_t *src, const int32_t *dst, int64_t n, void *workspace,
+                 int64_t workspace_bytes, int32_t *d_status, bwta_stream_t stream);
+
+/* Move the pages in use to the front of the pool, in every layer: with n of
+ * them in use, the k-th one numbered n or more goes to the k-th free page
+ * numbered below n. The table follows; *n_used (device int32, may be NULL) is n.
+ * What the pages past n hold is left as it was. */
+int bwta_kv_compact(const bwta_kv_cache *caches, int64_t n_layers, const bwta_kv_table *table,
+                    int32_t *n_used, void *workspace, int64_t workspace_bytes, int32_t *d_status,
+                    bwta_stream_t stream);
+
+/* Copy page src_pages[i] of every layer of src to page dst_pages[i] of dst (the
+ * same geometry, but for num_pages; src and dst may be the same pool). The
+ * copies happen at once: refused as BAD_PAGE, without effect, are pages out of
+ * range, every copy to a page that the list writes more than once, and, within
+ * one pool, every copy from a page that the list writes (other than onto
+ * itself).
+ *  src_pages, dst_pages   device int32 [n], n <= BWTA_KV_MAX_POOL
+ *  workspace  bwta_kv_pages_workspace(0, n) bytes */
+int bwta_kv_copy_pages(const bwta_kv_cache *src, const bwta_kv_cache *dst, int64_t n_layers,
+                       const int32_t *src_pages, const int32_t *dst_pages, int64_t n,
+                       void *workspace, int64_t workspace_bytes, int32_t *d_status,
+                       bwta_stream_t stream);
+int64_t bwta_kv_pages_workspace(int64_t num_pages, int64_t n);
+
 /* Failure-path self-test of the bounded waits. The paper has no counterpart:
  * this exercises the library's own error handling. It runs the tiled kernel of
  * bwta_gemm (arguments as there; M must be > 8) with one extra wait per CTA, on
