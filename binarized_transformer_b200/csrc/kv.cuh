@@ -106,6 +106,8 @@ struct KvTableView {
   int32_t max_pages, n_slots;
 };
 
+int64_t attn_decode_ws(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
+cudaError_t launch_attn_decode(const AttnArgs &a, bool e4m3, float *ws, cudaStream_t s);
 int64_t kv_pages_ws_ints(int64_t num_pages, int64_t n);
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
 cudaError_t launch_attn_simple(const AttnArgs &a, bool e4m3, cudaStream_t s);

@@ -216,10 +216,8 @@ int bwta_kv_append(const bwta_kv_cache *cache, const bwta_kv_table *table, const
 }
 
 int64_t bwta_attn_decode_workspace(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
-  (void)n_heads;
-  (void)n_kv_heads;
-  (void)head_dim;
-  return 0;
+  if (n_heads < 1 || n_kv_heads < 1 || head_dim < 1) return 0;
+  return attn_decode_ws(n_heads, n_kv_heads, head_dim);
 }
 
 int bwta_attn_decode_paged(const bwta_kv_cache *cache, const bwta_kv_table *table,
@@ -235,7 +233,9 @@ int bwta_attn_decode_paged(const bwta_kv_cache *cache, const bwta_kv_table *tabl
                               bwta_attn_decode_workspace(n_heads, cache->n_kv_heads, cache->head_dim)))
     return r;
   if (n_seq == 0) return BWTA_OK;
-  return cuda_status(launch_attn_simple(a, cache->type == BWTA_KV_E4M3, (cudaStream_t)stream));
+  if (n_seq * ((n_heads + 7) / 8) > I32_MAX) return BWTA_ERR_UNSUPPORTED;
+  return cuda_status(launch_attn_decode(a, cache->type == BWTA_KV_E4M3, static_cast<float *>(workspace),
+                                        (cudaStream_t)stream));
 }
 
 int bwta_attn_prompt_paged(const bwta_kv_cache *cache, const bwta_kv_table *table,
