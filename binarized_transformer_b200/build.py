@@ -26,7 +26,7 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcomp
                 "-I", os.path.join(ROOT, "include")]
 
 LIB_SOURCES = ["pack.cu", "gemm.cu", "decode.cu", "gemm_tc.cu", "attn.cu", "billm.cu", "billm_tc.cu",
-               "kv_append.cu", "kv_pages.cu", "attn_paged.cu", "attn_decode.cu",
+               "kv_append.cu", "kv_pages.cu", "attn_prompt.cu", "attn_decode.cu",
                "kv_abi.cu", "abi.cu"]
 MB_SOURCES = ["microbench.cu"]
 HEADERS = ["common.cuh", "tma.cuh", "quant.cuh", "tcgen05.cuh", "kv.cuh"]

@@ -1,0 +1,605 @@
+// attn_prompt.cu -- attention of many new tokens of each sequence over the paged
+// key-value cache, on the fifth-generation tensor cores.
+//
+// S = Q K^T and O = P V with P = 2^(S c - m), c = softmax_scale * log2(e). The rows
+// of a tile of 128 are R = 128 / G tokens times the G query heads that share a key
+// head, so keys and values are fetched (and E4M3 ones converted) once for all of
+// them, and a tile with many shared heads spans few positions: little of it is
+// hidden at the diagonal. A block owns two such tiles of one sequence and key head
+// and walks their visible key tiles of 128 tokens; the tensor cores work on one
+// tile's products while the other tile's softmax runs.
+//
+// The running reference m of a row follows its maximum only when a score passes it
+// by more than 2^8: until then weights up to 2^8 (of fp16's 2^16) are kept, and
+// the output in TMEM does not have to be rescaled. Sums and outputs are fp32; P is
+// rounded to fp16, its sum is not.
+//
+// Warps: 0-3 and 4-7 the softmax of tiles 0 and 1 (a thread a row), 8-11 keys and
+// values into shared memory (fp16: asynchronous 16-byte copies; E4M3: loaded,
+// converted and scaled, exact in fp16, and stored), 12 issues the MMAs. P
+// overwrites S in TMEM (A operand of the second product), in two halves that the
+// MMAs take up as they come. Keys and values lie in the same layout (128 rows of
+// 64 values, 128-byte swizzle, one after another for each 64 of D): K is read
+// along D, V across it (MN-major).
+//
+// Rows of the cache that no row of the block sees are never read: zeros stand in
+// their place (a weight of 0 times a NaN would be one). Every wait is bounded; on a
+// timeout the block flags it, lets its copies and MMAs finish, frees TMEM and returns.
+#include <algorithm>
+
+#include "kv.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace bwta {
+
+constexpr int PR_T = 128;           // rows of a tile, tokens of a key tile
+constexpr int PR_THREADS = 512;
+constexpr int PR_LAG = 2;           // key or value tiles whose copies are in flight
+constexpr float PR_SLACK = 8.0f;    // how far scores may pass the reference (log2)
+// Registers by role: 2 x 184 + 104 + 40 = 512 = the block's 65536 / 128.
+constexpr int PR_REG_SOFTMAX = 184, PR_REG_LOAD = 104, PR_REG_MMA = 40;
+
+template <int DP>
+struct PrShape {
+  static constexpr int NH = DP / 64;                  // halves of 64 columns
+  static constexpr int TILE = NH * PR_T * 128;        // bytes of 128 rows
+  static constexpr int SLOTS = DP == 128 ? 5 : 8;     // key and value tiles in the ring
+  static constexpr int SMEM = 1024 + (2 + SLOTS) * TILE + 1024;
+};
+
+struct PrArgs {
+  AttnArgs a;
+  int group, R;      // query heads of a key head, tokens of a tile
+};
+
+struct PrItem {
+  int64_t row0;        // of the pair's first token
+  int32_t slot, head;  // key head
+  int32_t cnt[2];      // tokens of each tile
+  int32_t pmin[2];     // position of a tile's first token (may be negative)
+  int32_t last[2], first[2], sink[2];  // its visible key tiles: [0, sink) and [first, last]; last < 0: none
+  int32_t u_sink, u_first, steps;      // the walk: [0, u_sink), then from u_first on
+  int32_t lo, hi;      // tokens that some row sees: [lo, hi] and those below the sinks
+  bool live;
+};
+
+struct PrBars {
+  uint64_t full[8], empty[8];
+  uint64_t q_ready;
+  uint64_t s_ready[2], p_ready[2][2], o_done[2], drain;
+  uint32_t tmem_base;
+  int32_t timeout, undrained;
+  PrItem item;
+};
+
+__device__ __forceinline__ bool pr_wait(PrBars *b, uint64_t *bar, uint32_t parity) {
+  if (*(volatile int32_t *)&b->timeout) return false;
+  if (mbar_wait(bar, parity)) return true;
+  b->timeout = 1;
+  return false;
+}
+
+__device__ __forceinline__ int pr_tile(const PrItem &it, int j) {
+  return j < it.u_sink ? j : it.u_first + j - it.u_sink;
+}
+__device__ __forceinline__ bool pr_active(const PrItem &it, int a, int t) {
+  return t <= it.last[a] && (t >= it.first[a] || t < it.sink[a]);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Block -> sequence, key head and pair of tiles. The pairs of a (sequence, head)
+// follow one another, the last (longest) first: their blocks run side by side
+// and share the keys in L2. Called by one warp.
+__device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
+  const AttnArgs &a = A.a;
+  const int lane = threadIdx.x % 32;
+  const int64_t at = blockIdx.x, H = a.c.H, two = 2 * A.R;
+  int64_t before = 0;
+  it.live = false;
+  for (int64_t s0 = 0; s0 < a.n_seq; s0 += 32) {
+    const int64_t s = s0 + lane;
+    int64_t c0 = 0, c1 = 0;
+    if (s < a.n_seq) {
+      c0 = min(max((int64_t)a.cu_q[s], (int64_t)0), a.total_q);
+      c1 = min(max((int64_t)a.cu_q[s + 1], c0), a.total_q);
+    }
+    const int64_t pairs = (c1 - c0 + two - 1) / two;
+    int64_t x = pairs * H;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(FULL, x, d);
+      if (lane >= d) x += y;
+    }
+    const unsigned hit = __ballot_sync(FULL, before + x > at);
+    if (!hit) {
+      before += __shfl_sync(FULL, x, 31);
+      continue;
+    }
+    if (lane == __ffs(hit) - 1) {
+      const int64_t local = at - (before + x - pairs * H);
+      const int64_t head = local / pairs, pair = pairs - 1 - (local - head * pairs);
+      const int64_t n = c1 - c0;
+      bool bad = false;
+      it.slot = kv_slot(a.r, s);
+      const int64_t len = kv_length(a.r, it.slot, a.c.ps, bad);
+      if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
+      it.head = (int32_t)head;
+      it.row0 = c0 + pair * two;
+      it.steps = 0;
+      int64_t pmax_all = -1, pmin_all = 0;
+      int32_t u_last = -1, u_first = 0x7fffffff, u_sink = 0;
+      for (int i = 0; i < 2; ++i) {
+        const int64_t tok = pair * two + i * A.R;
+        const int64_t cnt = min(max(n - tok, (int64_t)0), (int64_t)A.R);
+        const int64_t pmin = len - n + tok, pmax = pmin + cnt - 1;
+        it.cnt[i] = (int32_t)cnt;
+        it.pmin[i] = (int32_t)max(pmin, (int64_t)-256);  // 256 rows at most follow: all of them negative
+        it.last[i] = -1;
+        it.first[i] = it.sink[i] = 0;
+        if (cnt == 0 || pmax < 0) continue;
+        const int64_t lo = a.window ? max((int64_t)0, pmin - a.window + 1) : 0;
+        it.last[i] = (int32_t)(pmax / PR_T);
+        it.first[i] = (int32_t)(lo / PR_T);
+        it.sink[i] = (int32_t)min((a.sinks + PR_T - 1) / PR_T, lo / PR_T);
+        if (u_last < 0) pmin_all = pmin;
+        pmax_all = pmax;
+        u_last = max(u_last, it.last[i]);
+        u_first = min(u_first, it.first[i]);
+        u_sink = max(u_sink, it.sink[i]);
+      }
+      if (u_last >= 0) {
+        it.u_sink = min(u_sink, u_first);
+        it.u_first = u_first;
+        it.steps = it.u_sink + u_last - u_first + 1;
+        it.lo = (int32_t)(a.window ? max((int64_t)0, pmin_all - a.window + 1) : 0);
+        it.hi = (int32_t)pmax_all;
+      }
+      it.live = true;
+    }
+    return;
+  }
+}
+
+// Eight E4M3 bytes as halves times their row's scale (both exact in fp16).
+__device__ __forceinline__ uint4 pr_convert(uint2 b, uint32_t scale2) {
+  auto two = [&](uint32_t x) {
+    uint32_t h, r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(scale2));
+    return r;
+  };
+  return make_uint4(two(b.x & 0xffffu), two(b.x >> 16), two(b.y & 0xffffu), two(b.y >> 16));
+}
+
+__device__ __forceinline__ float pr_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int DP, bool E4M3>
+__global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
+  using S = PrShape<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  PrBars *bars = reinterpret_cast<PrBars *>(base + (2 + S::SLOTS) * S::TILE);
+  const AttnArgs &a = A.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, D = a.c.D;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::SLOTS; ++i) {
+      mbar_init(&bars->full[i], 4);
+      mbar_init(&bars->empty[i], 1);
+    }
+    mbar_init(&bars->q_ready, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_ready[i], 1);
+      mbar_init(&bars->p_ready[i][0], 4);
+      mbar_init(&bars->p_ready[i][1], 4);
+      mbar_init(&bars->o_done[i], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->timeout = bars->undrained = 0;
+    mbar_fence_init();
+  }
+  if (D % 16 != 0) {  // the products read 8 columns past D, which are never written: zero once
+    for (int i = threadIdx.x * 16; i < (2 + S::SLOTS) * S::TILE; i += PR_THREADS * 16)
+      *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 12) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (warp == 0) pr_find(A, bars->item);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const PrItem &it = bars->item;
+  // TMEM columns: S0 0, S1 128, O0 256, O1 384 (P of a tile: the first 64 of its S)
+  const int steps = it.live ? it.steps : 0;
+
+  if (warp < 8) {
+    // ------------------------------------------------ softmax and output
+    regs_inc<PR_REG_SOFTMAX>();
+    const int w = warp / 4, q = warp % 4, r = q * 32 + lane;
+    if (it.live) {
+      const int chunks = D / 8;
+      // Q rows of this tile, into the layout of the keys
+      uint8_t *qs = base + w * S::TILE;
+      const int used = it.cnt[w] * A.group;
+      const uint16_t *src = a.q + (it.row0 + (int64_t)w * A.R) * a.ldq + (int64_t)it.head * A.group * D;
+      for (int p = threadIdx.x % 128; p < PR_T * chunks; p += 128) {
+        const int rr = p / chunks, c = p - rr * chunks, tok = rr / A.group;
+        const uint16_t *from = src + (int64_t)tok * a.ldq + (int64_t)(rr - tok * A.group) * D + c * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (rr < used) v = *reinterpret_cast<const uint4 *>(from);
+        *reinterpret_cast<uint4 *>(qs + (c / 8) * (PR_T * 128) + swz128(rr, c % 8)) = v;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_ready);
+
+      const int tok = r / A.group;
+      const int p = it.pmin[w] + tok;
+      const bool valid = r < used;
+      const int64_t lo64 = a.window ? (int64_t)p - a.window + 1 : 0;
+      const int p_min = it.pmin[w], p_max = it.pmin[w] + it.cnt[w] - 1;
+      const float c2 = a.scale * 1.44269504088896340736f;
+      float m = -INFINITY, l = 0.0f;
+      bool first = true, ok = true;
+      uint32_t phase = 0;
+      const uint32_t ts = tmem_addr(tmem, q * 32, w * 128), to = tmem_addr(tmem, q * 32, 256 + w * 128);
+      for (int j = 0; j < steps; ++j) {
+        const int t = pr_tile(it, j), j0 = t * PR_T;
+        if (!pr_active(it, w, t)) continue;
+        ok = __all_sync(FULL, pr_wait(bars, &bars->s_ready[w], phase));
+        if (!ok) break;
+        phase ^= 1;
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, v[c]);
+        tmem_wait_ld();
+        const bool all = j0 + PR_T - 1 <= p_min &&
+                         (!a.window || j0 > p_max - a.window || j0 + PR_T <= a.sinks);
+        if (!all) {
+          const int hi = valid ? min(p - j0, PR_T) : -1;
+          const int lo = (int)min(max(lo64 - j0, (int64_t)-1), (int64_t)PR_T + 1);
+          const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_T + 1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int x = c * 32 + i;
+              if (x > hi || (x < lo && x >= sk)) v[c][i] = 0xff800000u;
+            }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(v[c][i]));
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
+        const bool up = mx > m + PR_SLACK || (m == -INFINITY && mx > m);
+        if (__any_sync(FULL, up)) {
+          const float mn = up ? mx : m;
+          // nothing seen so far: the sums are zero and the factor does not matter
+          const float f = m == -INFINITY ? 0.0f : pr_exp2(m - mn);
+          m = mn;
+          l *= f;
+          if (!first) {  // S being ready, the MMAs before it are complete: O holds still
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(to + c * 32, o);
+            }
+          }
+        }
+        first = false;
+        const float z = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = h * 2 + i / 16, e = (i % 16) * 2;
+            const float x = pr_exp2(fmaf(__uint_as_float(v[c][e]), c2, -z));
+            const float y = pr_exp2(fmaf(__uint_as_float(v[c][e + 1]), c2, -z));
+            sum[i % 2] += x;
+            sum[2 + i % 2] += y;
+            const __half2 two = __floats2half2_rn(x, y);
+            pk[i] = *reinterpret_cast<const uint32_t *>(&two);
+          }
+          tmem_st32(ts + h * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_ready[w][h]);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      // output
+      uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R + tok) * a.ldo +
+                      ((int64_t)it.head * A.group + (r - tok * A.group)) * D;
+      bool finite = true;
+      if (it.last[w] >= 0 && ok) ok = __all_sync(FULL, pr_wait(bars, &bars->o_done[w], 0));
+      if (ok) {
+        tc_fence_after();
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a row that sees nothing: zeros
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) {
+          if (c * 32 >= D) break;
+          uint32_t o[32];
+          if (it.last[w] >= 0) {
+            tmem_ld32(to + c * 32, o);
+            tmem_wait_ld();
+          }
+          if (!valid) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (c * 32 + i * 8 >= D) break;
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = inv == 0.0f ? 0.0f : __uint_as_float(o[i * 8 + 2 * e]) * inv;
+              const float y = inv == 0.0f ? 0.0f : __uint_as_float(o[i * 8 + 2 * e + 1]) * inv;
+              finite &= x - x == 0.0f && y - y == 0.0f;
+              const __half2 two = __floats2half2_rn(x, y);
+              h[e] = *reinterpret_cast<const uint32_t *>(&two);
+            }
+            *reinterpret_cast<uint4 *>(out + c * 32 + i * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+      }
+      if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------ keys and values
+    regs_dec<PR_REG_LOAD>();
+    constexpr int ITER = DP / 16;  // 16-byte chunks of fp16 a lane holds of 16 rows
+    const int chunks = D / 8, n = 2 * steps;
+    const uint32_t recip = 65536u / chunks + 1;  // p / chunks = (p * recip) >> 16 for p < 256
+    bool bad = false;
+    const uint32_t w2 = warp - 8;
+    // tile u (keys and values in turn), 16 tokens at a time: the offset of the first (in
+    // elements; scales: in floats), which of the 16 rows to read
+    struct Place {
+      int64_t at, sat;
+      uint32_t rows;
+    };
+    auto place = [&](int u, int gi) -> Place {
+      const int tok = pr_tile(it, u / 2) * PR_T + (w2 * 2 + gi) * 16;
+      Place p{0, 0, 0};
+      // bit r: token tok + r is seen by some row
+      const int top = min(it.hi - tok + 1, 16);
+      if (top <= 0) return p;
+      p.rows = (1u << top) - 1;
+      if (a.window && tok < it.lo) {
+        const uint32_t win = it.lo - tok >= 16 ? 0u : 0xffffu << (it.lo - tok);
+        const int64_t sk = a.sinks - tok;
+        p.rows &= win | (sk >= 16 ? 0xffffu : sk <= 0 ? 0u : (1u << sk) - 1);
+        if (!p.rows) return p;
+      }
+      const int idx = tok / a.c.ps, in = tok - idx * a.c.ps;
+      const int32_t page = a.r.pages[(int64_t)it.slot * a.r.ld + idx];
+      if ((uint32_t)page >= (uint32_t)a.c.num_pages) {
+        bad = true;
+        p.rows = 0;
+        return p;
+      }
+      const int64_t row = (int64_t)it.head * a.c.ps + in;
+      p.at = (int64_t)page * a.c.page_stride + row * D;
+      p.sat = (int64_t)page * a.c.scale_stride + row;
+      return p;
+    };
+    auto slot_of = [&](int u) { return base + (2 + u % S::SLOTS) * S::TILE; };
+    auto arrive = [&](int u) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->full[u % S::SLOTS]);
+    };
+    auto dst_of = [&](int gi, int p) -> uint32_t {
+      const int r = (int)((p * recip) >> 16), c = p - r * chunks;
+      return (uint32_t)((c / 8) * (PR_T * 128)) + swz128((w2 * 2 + gi) * 16 + r, c % 8);
+    };
+    bool ok = true;
+    if (!E4M3) {
+      int u = 0;
+      for (; u < n && ok; ++u) {
+        Place pl[2] = {place(u, 0), place(u, 1)};
+        if (u >= S::SLOTS) ok = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        const uint32_t st = smem_addr(slot_of(u));
+        const uint16_t *kv = reinterpret_cast<const uint16_t *>(u & 1 ? a.c.v : a.c.k);
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi)
+#pragma unroll
+          for (int i = 0; i < ITER; ++i) {
+            const int p = i * 32 + lane;
+            if (p < 16 * chunks) {
+              const int r = (int)((p * recip) >> 16);
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + dst_of(gi, p)),
+                           "l"(kv + pl[gi].at + p * 8), "r"((pl[gi].rows >> r) & 1 ? 16 : 0)
+                           : "memory");
+            }
+          }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (u >= PR_LAG) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(PR_LAG) : "memory");
+          arrive(u - PR_LAG);
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (ok)
+        for (int v = max(0, n - PR_LAG); v < n; ++v) arrive(v);
+    } else {
+      uint2 raw[2][2][ITER];
+      float sc[2][2];
+      auto fetch = [&](int u, uint2 (&x)[2][ITER], float (&s)[2]) {
+        const uint8_t *kv = u & 1 ? a.c.v : a.c.k;
+        const float *ss = u & 1 ? a.c.vs : a.c.ks;
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi) {
+          const Place pl = place(u, gi);
+          s[gi] = (pl.rows >> (lane & 15)) & 1 ? ss[pl.sat + (lane & 15)] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < ITER; ++i) {
+            const int p = i * 32 + lane;
+            x[gi][i] = make_uint2(0, 0);
+            if (p < 16 * chunks && ((pl.rows >> ((p * recip) >> 16)) & 1))
+              x[gi][i] = *reinterpret_cast<const uint2 *>(kv + pl.at + p * 8);
+          }
+        }
+      };
+      auto store = [&](int u, const uint2 (&x)[2][ITER], const float (&s)[2]) -> bool {
+        bool fine = true;
+        if (u >= S::SLOTS) fine = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
+        if (!__all_sync(FULL, fine)) return false;
+        uint8_t *st = slot_of(u);
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi) {
+          const uint32_t h = (uint32_t)__half_as_ushort(__float2half_rn(s[gi]));
+#pragma unroll
+          for (int i = 0; i < ITER; ++i) {
+            const int p = i * 32 + lane;
+            const uint32_t one = __shfl_sync(FULL, h, ((p * recip) >> 16) & 15);
+            if (p < 16 * chunks)
+              *reinterpret_cast<uint4 *>(st + dst_of(gi, p)) = pr_convert(x[gi][i], one | (one << 16));
+          }
+        }
+        arrive(u);
+        return true;
+      };
+      if (n > 0) fetch(0, raw[0], sc[0]);
+      for (int u = 0; u < n && ok; u += 2) {  // n is even
+        fetch(u + 1, raw[1], sc[1]);
+        ok = store(u, raw[0], sc[0]);
+        if (!ok) break;
+        if (u + 2 < n) fetch(u + 2, raw[0], sc[0]);
+        ok = store(u + 1, raw[1], sc[1]);
+      }
+    }
+    if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
+  } else {
+    // ------------------------------------------------ MMA issue
+    regs_dec<PR_REG_MMA>();
+    if (warp == 12 && lane == 0 && steps > 0) {
+      const uint32_t id_qk = idesc_f16_f32(PR_T, PR_T);
+      const uint32_t id_pv = idesc_f16_f32(PR_T, (D + 15) / 16 * 16) | IDESC_B_MN;
+      const int ks = (D + 15) / 16;
+      const uint32_t s0 = smem_addr(base);
+      uint32_t p_phase[2] = {0, 0};
+      bool ok = pr_wait(bars, &bars->q_ready, 0);
+      auto slot = [&](int u) { return s0 + (2 + u % S::SLOTS) * S::TILE; };
+      auto full = [&](int u) { return pr_wait(bars, &bars->full[u % S::SLOTS], (u / S::SLOTS) & 1); };
+      auto qk = [&](int w, int j) {
+        const uint32_t qa = s0 + w * S::TILE, kb = slot(2 * j);
+        for (int k = 0; k < ks; ++k) {
+          const uint32_t off = (k / 4) * (PR_T * 128) + (k % 4) * 32;
+          mma_f16_ss(tmem + w * 128, smem_desc_k_sw128(qa + off), smem_desc_k_sw128(kb + off), id_qk, k > 0);
+        }
+        tc_commit(&bars->s_ready[w]);
+      };
+      bool began[2] = {false, false};
+      // the first keys
+      if (ok) ok = full(0);
+      if (ok) {
+        tc_fence_after();
+        for (int w = 0; w < 2; ++w)
+          if (pr_active(it, w, pr_tile(it, 0))) qk(w, 0);
+        tc_commit(&bars->empty[0]);
+      }
+      for (int j = 0; j < steps && ok; ++j) {
+        const int t = pr_tile(it, j), tn = j + 1 < steps ? pr_tile(it, j + 1) : 0x7fffffff;
+        ok = full(2 * j + 1);
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (pr_active(it, w, t)) {
+            const uint32_t vb = slot(2 * j + 1);
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = pr_wait(bars, &bars->p_ready[w][h], p_phase[w]);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + (h * 4 + k) * 8,
+                           smem_desc_mn_sw128(vb + (h * 4 + k) * 2048, PR_T * 128), id_pv, began[w]);
+                began[w] = true;
+              }
+            }
+            p_phase[w] ^= 1;
+            if (t == it.last[w] && ok) tc_commit(&bars->o_done[w]);
+          }
+          if (ok && j + 1 < steps && pr_active(it, w, tn)) {
+            ok = full(2 * j + 2);
+            if (ok) {
+              tc_fence_after();
+              qk(w, j + 1);
+            }
+          }
+        }
+        if (!ok) break;
+        tc_commit(&bars->empty[(2 * j + 1) % S::SLOTS]);
+        if (j + 1 < steps) tc_commit(&bars->empty[(2 * j + 2) % S::SLOTS]);
+      }
+      // every MMA has completed before TMEM is released
+      tc_commit(&bars->drain);
+      if (!mbar_wait(&bars->drain, 0, DRAIN_NS)) bars->undrained = 1;
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && bars->timeout)
+    flag_status(a.d_status, BWTA_STATUS_TIMEOUT | (bars->undrained ? BWTA_STATUS_DRAIN : 0));
+}
+
+int64_t attn_prompt_blocks(int64_t n_seq, int64_t total_q, int64_t n_heads, int64_t n_kv_heads) {
+  const int64_t two = 2 * (PR_T / (n_heads / n_kv_heads));
+  return n_kv_heads * (total_q / two + std::min(n_seq, total_q));  // a sum of rounded-up quotients at most
+}
+
+template <int DP, bool E4M3>
+static cudaError_t launch_prompt_t(const PrArgs &A, int64_t blocks, cudaStream_t s) {
+  static SmemOptIn opt_in;
+  auto kern = k_attn_prompt<DP, E4M3>;
+  if (cudaError_t e = opt_in(kern, PrShape<DP>::SMEM)) return e;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PR_THREADS), PrShape<DP>::SMEM, s, A);
+}
+
+cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
+  PrArgs A = {};
+  A.a = a;
+  A.group = a.n_heads / a.c.H;
+  A.R = PR_T / A.group;
+  const int64_t blocks = attn_prompt_blocks(a.n_seq, a.total_q, a.n_heads, a.c.H);
+  if (a.c.D <= 64)
+    return e4m3 ? launch_prompt_t<64, true>(A, blocks, s) : launch_prompt_t<64, false>(A, blocks, s);
+  return e4m3 ? launch_prompt_t<128, true>(A, blocks, s) : launch_prompt_t<128, false>(A, blocks, s);
+}
+
+}  // namespace bwta

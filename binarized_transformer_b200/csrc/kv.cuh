@@ -110,7 +110,8 @@ int64_t attn_decode_ws(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
 cudaError_t launch_attn_decode(const AttnArgs &a, bool e4m3, float *ws, cudaStream_t s);
 int64_t kv_pages_ws_ints(int64_t num_pages, int64_t n);
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
-cudaError_t launch_attn_simple(const AttnArgs &a, bool e4m3, cudaStream_t s);
+int64_t attn_prompt_blocks(int64_t n_seq, int64_t total_q, int64_t n_heads, int64_t n_kv_heads);
+cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s);
 cudaError_t launch_kv_reserve(const KvTableView &t, int32_t num_pages, int32_t ps,
                               const int32_t *slots, const int32_t *n_new, int32_t n,
                               int32_t *d_status, cudaStream_t s);

@@ -250,7 +250,8 @@ int bwta_attn_prompt_paged(const bwta_kv_cache *cache, const bwta_kv_table *tabl
     return r;
   if (n_heads / cache->n_kv_heads > 128) return BWTA_ERR_UNSUPPORTED;
   if (n_seq == 0 || total_q == 0) return BWTA_OK;
-  return cuda_status(launch_attn_simple(a, cache->type == BWTA_KV_E4M3, (cudaStream_t)stream));
+  if (attn_prompt_blocks(n_seq, total_q, n_heads, cache->n_kv_heads) > I32_MAX) return BWTA_ERR_UNSUPPORTED;
+  return cuda_status(launch_attn_prompt(a, cache->type == BWTA_KV_E4M3, (cudaStream_t)stream));
 }
 
 int bwta_kv_reserve(const bwta_kv_table *table, int64_t num_pages, int64_t page_size,

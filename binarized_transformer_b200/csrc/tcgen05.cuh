@@ -101,6 +101,30 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Bit of an instruction descriptor: B is stored MN-major (its rows run along N).
+constexpr uint32_t IDESC_B_MN = 1u << 16;
+
+// Descriptor of an MN-major operand tile with the 128-byte swizzle: rows of one k
+// and 64 16-bit values along MN (128 bytes), 8 rows (1024 bytes) an atom, atoms
+// along k one after another (stride offset 1024), the next 64 values of MN
+// `mn_stride` bytes further (leading-dimension offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(mn_stride >> 4) << 16) |
+         ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// D[tmem] (+)= A[tmem] x B[smem desc]^T, kind::f16: A two halves a column, 8 columns
+// an instruction.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // D[tmem] (+)= A[smem desc] x B[smem desc]^T, kind::f16 (K = 16 per instruction).
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
