@@ -14,9 +14,11 @@
 // the output in TMEM does not have to be rescaled. Sums and outputs are fp32; P is
 // rounded to fp16, its sum is not.
 //
-// Warps: 0-3 and 4-7 the softmax of tiles 0 and 1 (a thread a row), 8-11 keys and
+// Warps: 8-11 and 12-15 the softmax of tiles 0 and 1 (a thread a row), 4-7 keys and
 // values into shared memory (fp16: asynchronous 16-byte copies; E4M3: loaded,
-// converted and scaled, exact in fp16, and stored), 12 issues the MMAs. P
+// converted and scaled, exact in fp16, and stored), 0 and 1 issue the MMAs of tile 0
+// and 1 (the lowest warps of their SM sub-partitions, which the others' arithmetic
+// then holds up least). P
 // overwrites S in TMEM (A operand of the second product), in two halves that the
 // MMAs take up as they come. Keys and values lie in the same layout (128 rows of
 // 64 values, 128-byte swizzle, one after another for each 64 of D): K is read
@@ -67,7 +69,7 @@ struct PrItem {
 struct PrBars {
   uint64_t full[8], empty[8];
   uint64_t q_ready;
-  uint64_t s_ready[2], p_ready[2][2], o_done[2], drain;
+  uint64_t s_ready[2], p_ready[2][2], o_done[2], drain[2];
   uint32_t tmem_base;
   int32_t timeout, undrained;
   PrItem item;
@@ -75,7 +77,25 @@ struct PrBars {
 
 __device__ __forceinline__ bool pr_wait(PrBars *b, uint64_t *bar, uint32_t parity) {
   if (*(volatile int32_t *)&b->timeout) return false;
-  if (mbar_wait(bar, parity)) return true;
+  // no suspend-time hint: these waits are short and follow one another in a chain
+  const uint32_t at = smem_addr(bar);
+  uint64_t t0 = 0;
+  for (int i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (i % 64 == 63) {
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > 2000000000ull) break;
+    }
+  }
   b->timeout = 1;
   return false;
 }
@@ -200,7 +220,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
       mbar_init(&bars->full[i], 4);
-      mbar_init(&bars->empty[i], 1);
+      mbar_init(&bars->empty[i], 2);
     }
     mbar_init(&bars->q_ready, 8);
     for (int i = 0; i < 2; ++i) {
@@ -208,8 +228,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       mbar_init(&bars->p_ready[i][0], 4);
       mbar_init(&bars->p_ready[i][1], 4);
       mbar_init(&bars->o_done[i], 1);
+      mbar_init(&bars->drain[i], 1);
     }
-    mbar_init(&bars->drain, 1);
     bars->timeout = bars->undrained = 0;
     mbar_fence_init();
   }
@@ -218,12 +238,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == 0) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
   pdl_wait();
-  if (warp == 0) pr_find(A, bars->item);
+  if (warp == 4) pr_find(A, bars->item);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,10 +252,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
   // TMEM columns: S0 0, S1 128, O0 256, O1 384 (P of a tile: the first 64 of its S)
   const int steps = it.live ? it.steps : 0;
 
-  if (warp < 8) {
+  if (warp >= 8) {
     // ------------------------------------------------ softmax and output
     regs_inc<PR_REG_SOFTMAX>();
-    const int w = warp / 4, q = warp % 4, r = q * 32 + lane;
+    const int w = warp / 4 - 2, q = warp % 4, r = q * 32 + lane;
     if (it.live) {
       const int chunks = D / 8;
       // Q rows of this tile, into the layout of the keys
@@ -277,6 +297,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         const bool all = j0 + PR_T - 1 <= p_min &&
                          (!a.window || j0 > p_max - a.window || j0 + PR_T <= a.sinks);
         if (!all) {
+          asm volatile("");  // a branch, not selects in every tile
           const int hi = valid ? min(p - j0, PR_T) : -1;
           const int lo = (int)min(max(lo64 - j0, (int64_t)-1), (int64_t)PR_T + 1);
           const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_T + 1);
@@ -303,13 +324,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
           l *= f;
           if (!first) {  // S being ready, the MMAs before it are complete: O holds still
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + c * 32, o);
+            for (int c = 0; c < DP / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + c * 16, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(to + c * 32, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(to + c * 16, o);
             }
           }
         }
@@ -372,22 +393,28 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       }
       if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
     }
-  } else if (warp < 12) {
+  } else if (warp >= 4) {
     // ------------------------------------------------ keys and values
     regs_dec<PR_REG_LOAD>();
     constexpr int ITER = DP / 16;  // 16-byte chunks of fp16 a lane holds of 16 rows
     const int chunks = D / 8, n = 2 * steps;
     const uint32_t recip = 65536u / chunks + 1;  // p / chunks = (p * recip) >> 16 for p < 256
     bool bad = false;
-    const uint32_t w2 = warp - 8;
-    // tile u (keys and values in turn), 16 tokens at a time: the offset of the first (in
+    const uint32_t w2 = warp - 4;
+    // 16 tokens of key tile j (and their values): the offset of the first (in
     // elements; scales: in floats), which of the 16 rows to read
     struct Place {
       int64_t at, sat;
       uint32_t rows;
     };
-    auto place = [&](int u, int gi) -> Place {
-      const int tok = pr_tile(it, u / 2) * PR_T + (w2 * 2 + gi) * 16;
+    auto token = [&](int j, int gi) { return pr_tile(it, j) * PR_T + (int)(w2 * 2 + gi) * 16; };
+    // the page's number is fetched a tile ahead
+    auto page_of = [&](int j, int gi) -> int32_t {
+      const int tok = token(j, gi);
+      return j < steps && tok <= it.hi ? a.r.pages[(int64_t)it.slot * a.r.ld + tok / a.c.ps] : -1;
+    };
+    auto place = [&](int j, int gi, int32_t page) -> Place {
+      const int tok = token(j, gi);
       Place p{0, 0, 0};
       // bit r: token tok + r is seen by some row
       const int top = min(it.hi - tok + 1, 16);
@@ -399,14 +426,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         p.rows &= win | (sk >= 16 ? 0xffffu : sk <= 0 ? 0u : (1u << sk) - 1);
         if (!p.rows) return p;
       }
-      const int idx = tok / a.c.ps, in = tok - idx * a.c.ps;
-      const int32_t page = a.r.pages[(int64_t)it.slot * a.r.ld + idx];
       if ((uint32_t)page >= (uint32_t)a.c.num_pages) {
         bad = true;
         p.rows = 0;
         return p;
       }
-      const int64_t row = (int64_t)it.head * a.c.ps + in;
+      const int64_t row = (int64_t)it.head * a.c.ps + tok % a.c.ps;
       p.at = (int64_t)page * a.c.page_stride + row * D;
       p.sat = (int64_t)page * a.c.scale_stride + row;
       return p;
@@ -423,9 +448,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     };
     bool ok = true;
     if (!E4M3) {
-      int u = 0;
-      for (; u < n && ok; ++u) {
-        Place pl[2] = {place(u, 0), place(u, 1)};
+      Place pl[2];
+      int32_t page[2] = {page_of(0, 0), page_of(0, 1)};
+      for (int u = 0; u < n && ok; ++u) {  // keys and values of a tile in turn
+        if (!(u & 1)) {
+#pragma unroll
+          for (int gi = 0; gi < 2; ++gi) {
+            pl[gi] = place(u / 2, gi, page[gi]);
+            page[gi] = page_of(u / 2 + 1, gi);
+          }
+        }
         if (u >= S::SLOTS) ok = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
         ok = __all_sync(FULL, ok);
         if (!ok) break;
@@ -455,19 +487,24 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     } else {
       uint2 raw[2][2][ITER];
       float sc[2][2];
+      Place pl[2];
+      int32_t page[2] = {page_of(0, 0), page_of(0, 1)};
       auto fetch = [&](int u, uint2 (&x)[2][ITER], float (&s)[2]) {
         const uint8_t *kv = u & 1 ? a.c.v : a.c.k;
         const float *ss = u & 1 ? a.c.vs : a.c.ks;
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
-          const Place pl = place(u, gi);
-          s[gi] = (pl.rows >> (lane & 15)) & 1 ? ss[pl.sat + (lane & 15)] : 0.0f;
+          if (!(u & 1)) {
+            pl[gi] = place(u / 2, gi, page[gi]);
+            page[gi] = page_of(u / 2 + 1, gi);
+          }
+          s[gi] = (pl[gi].rows >> (lane & 15)) & 1 ? ss[pl[gi].sat + (lane & 15)] : 0.0f;
 #pragma unroll
           for (int i = 0; i < ITER; ++i) {
             const int p = i * 32 + lane;
             x[gi][i] = make_uint2(0, 0);
-            if (p < 16 * chunks && ((pl.rows >> ((p * recip) >> 16)) & 1))
-              x[gi][i] = *reinterpret_cast<const uint2 *>(kv + pl.at + p * 8);
+            if (p < 16 * chunks && ((pl[gi].rows >> ((p * recip) >> 16)) & 1))
+              x[gi][i] = *reinterpret_cast<const uint2 *>(kv + pl[gi].at + p * 8);
           }
         }
       };
@@ -503,74 +540,88 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
   } else {
     // ------------------------------------------------ MMA issue
     regs_dec<PR_REG_MMA>();
-    if (warp == 12 && lane == 0 && steps > 0) {
+    // warp w issues the products of tile w, all lanes in step
+    if (warp < 2 && steps > 0) {
+      const int w = warp, n = __shfl_sync(FULL, steps, 0);
+      const uint32_t on = lane == 0;
       const uint32_t id_qk = idesc_f16_f32(PR_T, PR_T);
       const uint32_t id_pv = idesc_f16_f32(PR_T, (D + 15) / 16 * 16) | IDESC_B_MN;
       const int ks = (D + 15) / 16;
-      const uint32_t s0 = smem_addr(base);
-      uint32_t p_phase[2] = {0, 0};
-      bool ok = pr_wait(bars, &bars->q_ready, 0);
-      auto slot = [&](int u) { return s0 + (2 + u % S::SLOTS) * S::TILE; };
-      auto full = [&](int u) { return pr_wait(bars, &bars->full[u % S::SLOTS], (u / S::SLOTS) & 1); };
-      auto qk = [&](int w, int j) {
-        const uint32_t qa = s0 + w * S::TILE, kb = slot(2 * j);
-        for (int k = 0; k < ks; ++k) {
-          const uint32_t off = (k / 4) * (PR_T * 128) + (k % 4) * 32;
-          mma_f16_ss(tmem + w * 128, smem_desc_k_sw128(qa + off), smem_desc_k_sw128(kb + off), id_qk, k > 0);
-        }
-        tc_commit(&bars->s_ready[w]);
+      const uint32_t s0 = __shfl_sync(FULL, smem_addr(base), 0);
+      const uint32_t ts = __shfl_sync(FULL, tmem, 0) + w * 128, to = ts + 256;
+      const uint64_t qa = smem_desc_k_sw128(s0 + w * S::TILE);
+      const uint64_t ring = smem_desc_k_sw128(s0 + 2 * S::TILE);
+      const uint64_t ring_mn = smem_desc_mn_sw128(s0 + 2 * S::TILE, PR_T * 128);
+      const int last = __shfl_sync(FULL, it.last[w], 0), first = __shfl_sync(FULL, it.first[w], 0);
+      const int sink = __shfl_sync(FULL, it.sink[w], 0);
+      const int u_sink = __shfl_sync(FULL, it.u_sink, 0), u_first = __shfl_sync(FULL, it.u_first, 0);
+      auto active = [&](int j) {
+        const int t = j < u_sink ? j : u_first + j - u_sink;
+        return t <= last && (t >= first || t < sink);
       };
-      bool began[2] = {false, false};
-      // the first keys
-      if (ok) ok = full(0);
-      if (ok) {
-        tc_fence_after();
-        for (int w = 0; w < 2; ++w)
-          if (pr_active(it, w, pr_tile(it, 0))) qk(w, 0);
-        tc_commit(&bars->empty[0]);
-      }
-      for (int j = 0; j < steps && ok; ++j) {
-        const int t = pr_tile(it, j), tn = j + 1 < steps ? pr_tile(it, j + 1) : 0x7fffffff;
-        ok = full(2 * j + 1);
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (pr_active(it, w, t)) {
-            const uint32_t vb = slot(2 * j + 1);
-            for (int h = 0; h < 2 && ok; ++h) {
-              ok = pr_wait(bars, &bars->p_ready[w][h], p_phase[w]);
+      auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, pr_wait(bars, bar, parity)); };
+      // keys of step j: slot and phase of tile 2 j, values: of 2 j + 1
+      int slot = 0;
+      uint32_t phase = 0, p_phase = 0, more = 0;
+      auto next = [&]() {
+        if (++slot == S::SLOTS) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      auto qk = [&]() {
+        const uint64_t kb = ring + (uint64_t)(slot * (S::TILE >> 4));
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          if (k >= ks) break;
+          const uint32_t off = ((k / 4) * (PR_T * 128) + (k % 4) * 32) >> 4;
+          mma_f16_ss_if(on, ts, qa + off, kb + off, id_qk, k > 0);
+        }
+        tc_commit_if(on, &bars->s_ready[w]);
+      };
+      bool ok = ready(&bars->q_ready, 0);
+      for (int j = 0; j <= n && ok; ++j) {
+        if (j > 0) {  // the values of step j - 1
+          ok = ready(&bars->full[slot], phase);
+          if (!ok) break;
+          if (active(j - 1)) {
+            const uint64_t vb = ring_mn + (uint64_t)(slot * (S::TILE >> 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && ready(&bars->p_ready[w][h], p_phase);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + (h * 4 + k) * 8,
-                           smem_desc_mn_sw128(vb + (h * 4 + k) * 2048, PR_T * 128), id_pv, began[w]);
-                began[w] = true;
+                mma_f16_ts_if(on, to, ts + (h * 4 + k) * 8, vb + (uint64_t)((h * 4 + k) * (2048 >> 4)), id_pv, more);
+                more = 1;
               }
             }
-            p_phase[w] ^= 1;
-            if (t == it.last[w] && ok) tc_commit(&bars->o_done[w]);
+            if (!ok) break;
+            p_phase ^= 1;
           }
-          if (ok && j + 1 < steps && pr_active(it, w, tn)) {
-            ok = full(2 * j + 2);
-            if (ok) {
-              tc_fence_after();
-              qk(w, j + 1);
-            }
-          }
+          tc_commit_if(on, j == n ? &bars->o_done[w] : &bars->empty[slot]);
+          next();
         }
-        if (!ok) break;
-        tc_commit(&bars->empty[(2 * j + 1) % S::SLOTS]);
-        if (j + 1 < steps) tc_commit(&bars->empty[(2 * j + 2) % S::SLOTS]);
+        if (j < n) {  // the keys of step j
+          ok = ready(&bars->full[slot], phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (active(j)) qk();
+          tc_commit_if(on, &bars->empty[slot]);
+          next();
+        }
       }
       // every MMA has completed before TMEM is released
-      tc_commit(&bars->drain);
-      if (!mbar_wait(&bars->drain, 0, DRAIN_NS)) bars->undrained = 1;
+      tc_commit_if(on, &bars->drain[w]);
+      if (!mbar_wait(&bars->drain[w], 0, DRAIN_NS)) bars->undrained = 1;
     }
     __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
