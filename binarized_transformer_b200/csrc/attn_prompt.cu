@@ -38,16 +38,20 @@ namespace bwta {
 constexpr int PR_T = 128;           // rows of a tile, tokens of a key tile
 constexpr int PR_THREADS = 512;
 constexpr int PR_LAG = 2;           // key or value tiles whose copies are in flight
+constexpr int PR_POLY = 4;          // one pair of weights in so many goes to the FMA units
 constexpr float PR_SLACK = 8.0f;    // how far scores may pass the reference (log2)
 // Registers by role: 2 x 184 + 104 + 40 = 512 = the block's 65536 / 128.
 constexpr int PR_REG_SOFTMAX = 184, PR_REG_LOAD = 104, PR_REG_MMA = 40;
 
-template <int DP>
+template <int DP, bool E4M3>
 struct PrShape {
   static constexpr int NH = DP / 64;                  // halves of 64 columns
   static constexpr int TILE = NH * PR_T * 128;        // bytes of 128 rows
-  static constexpr int SLOTS = DP == 128 ? 5 : 8;     // key and value tiles in the ring
-  static constexpr int SMEM = 1024 + (2 + SLOTS) * TILE + 1024;
+  static constexpr int SLOTS = DP == 128 ? (E4M3 ? 4 : 5) : 8;  // key and value tiles in the ring
+  static constexpr int RAW = E4M3 ? 16 * DP + 64 : 0;  // 16 rows as they lie in the cache, with their scales
+  static constexpr int BARS = 1024;
+  static constexpr int SMEM = 1024 + (2 + SLOTS) * TILE + 16 * RAW + BARS;
+  static_assert(SMEM <= 232448, "shared memory of a block");
 };
 
 struct PrArgs {
@@ -67,7 +71,7 @@ struct PrItem {
 };
 
 struct PrBars {
-  uint64_t full[8], empty[8];
+  uint64_t full[8], empty[8], raw[4][4], turn[2];
   uint64_t q_ready;
   uint64_t s_ready[2], p_ready[2][2], o_done[2], drain[2];
   uint32_t tmem_base;
@@ -206,13 +210,60 @@ __device__ __forceinline__ float pr_exp2(float x) {
   return y;
 }
 
+// Two fp32 numbers in a register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pk2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 up2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x for two numbers on the FMA units, for a part of a row's weights: the unit that
+// has the exponential takes 16 a clock, as long for a tile as the tensor cores.
+// x = n + f, n the nearest integer; 2^f on [-1/2, 1/2] by a polynomial of degree 5
+// (equal-ripple fit of the relative error, 7.5e-8), n added to the exponent. Below
+// -126 it stays 2^-126, nothing to fp16; a NaN ends as an infinite weight in fp16.
+__device__ __forceinline__ float2 pr_exp2_poly(uint64_t x) {
+  float2 v = up2(x);
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.x));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.y));
+  const uint64_t c = pk2(v.x, v.y), magic = pk2(12582912.0f, 12582912.0f);
+  const uint64_t r = add2(c, magic);                                     // 1.5 * 2^23 + n
+  const uint64_t nf = add2(r, pk2(-12582912.0f, -12582912.0f));
+  const uint64_t f = fma2(nf, pk2(-1.0f, -1.0f), c);
+  uint64_t p = pk2(0.0013276472f, 0.0013276472f);
+  p = fma2(p, f, pk2(0.0096755413f, 0.0096755413f));
+  p = fma2(p, f, pk2(0.0555071327f, 0.0555071327f));
+  p = fma2(p, f, pk2(0.2402211972f, 0.2402211972f));
+  p = fma2(p, f, pk2(0.6931469671f, 0.6931469671f));
+  p = fma2(p, f, pk2(1.0000000717f, 1.0000000717f));
+  const float2 n = up2(r), y = up2(p);
+  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(n.x) << 23)),
+                     __int_as_float(__float_as_int(y.y) + (__float_as_int(n.y) << 23)));
+}
+
 template <int DP, bool E4M3>
 __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
-  using S = PrShape<DP>;
+  using S = PrShape<DP, E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  PrBars *bars = reinterpret_cast<PrBars *>(base + (2 + S::SLOTS) * S::TILE);
+  PrBars *bars = reinterpret_cast<PrBars *>(base + (2 + S::SLOTS) * S::TILE + 16 * S::RAW);
+  static_assert(sizeof(PrBars) <= S::BARS, "barriers");
   const AttnArgs &a = A.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, D = a.c.D;
 
@@ -229,7 +280,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       mbar_init(&bars->p_ready[i][1], 4);
       mbar_init(&bars->o_done[i], 1);
       mbar_init(&bars->drain[i], 1);
+      mbar_init(&bars->turn[i], 4);
     }
+    for (int i = 0; i < 16; ++i) mbar_init(&bars->raw[i / 4][i % 4], 1);
     bars->timeout = bars->undrained = 0;
     mbar_fence_init();
   }
@@ -282,6 +335,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       float m = -INFINITY, l = 0.0f;
       bool first = true, ok = true;
       uint32_t phase = 0;
+      int turns = 0;  // steps in which both tiles took part
       const uint32_t ts = tmem_addr(tmem, q * 32, w * 128), to = tmem_addr(tmem, q * 32, 256 + w * 128);
       for (int j = 0; j < steps; ++j) {
         const int t = pr_tile(it, j), j0 = t * PR_T;
@@ -336,27 +390,46 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         }
         first = false;
         const float z = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0, 0, 0, 0};
+        // the two tiles take turns: side by side they would wait for the same units, and
+        // then for the tensor cores, both at once
+        const bool both = pr_active(it, 1 - w, t);
+        if (both && (w == 1 || turns > 0)) {
+          ok = __all_sync(FULL, pr_wait(bars, &bars->turn[w], (turns - 1 + w) & 1));
+          if (!ok) break;
+        }
+        const uint64_t cc = pk2(c2, c2), zz = pk2(-z, -z);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int c = h * 2 + i / 16, e = (i % 16) * 2;
-            const float x = pr_exp2(fmaf(__uint_as_float(v[c][e]), c2, -z));
-            const float y = pr_exp2(fmaf(__uint_as_float(v[c][e + 1]), c2, -z));
-            sum[i % 2] += x;
-            sum[2 + i % 2] += y;
-            const __half2 two = __floats2half2_rn(x, y);
+            const uint64_t x = fma2(pk2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), cc, zz);
+            float2 y;
+            if (i % PR_POLY == PR_POLY - 1) {
+              y = pr_exp2_poly(x);
+            } else {
+              y = up2(x);
+              y.x = pr_exp2(y.x);
+              y.y = pr_exp2(y.y);
+            }
+            sum[i % 2] = add2(sum[i % 2], pk2(y.x, y.y));
+            const __half2 two = __floats2half2_rn(y.x, y.y);
             pk[i] = *reinterpret_cast<const uint32_t *>(&two);
           }
           tmem_st32(ts + h * 32, pk);
+          if (h == 1 && both) {
+            if (lane == 0) mbar_arrive(&bars->turn[1 - w]);
+            ++turns;
+          }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->p_ready[w][h]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 sa = up2(add2(sum[0], sum[1]));
+        l += sa.x + sa.y;
       }
       // output
       uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R + tok) * a.ldo +
@@ -485,56 +558,78 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       if (ok)
         for (int v = max(0, n - PR_LAG); v < n; ++v) arrive(v);
     } else {
-      uint2 raw[2][2][ITER];
-      float sc[2][2];
-      Place pl[2];
+      // a ring of this warp's own: 16 rows of keys (twice) and of values (twice), each
+      // refilled for the next tile as soon as it has been converted
+      uint8_t *raw = base + (2 + S::SLOTS) * S::TILE + w2 * 4 * S::RAW;
       int32_t page[2] = {page_of(0, 0), page_of(0, 1)};
-      auto fetch = [&](int u, uint2 (&x)[2][ITER], float (&s)[2]) {
-        const uint8_t *kv = u & 1 ? a.c.v : a.c.k;
-        const float *ss = u & 1 ? a.c.vs : a.c.ks;
-#pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-          if (!(u & 1)) {
-            pl[gi] = place(u / 2, gi, page[gi]);
-            page[gi] = page_of(u / 2 + 1, gi);
-          }
-          s[gi] = (pl[gi].rows >> (lane & 15)) & 1 ? ss[pl[gi].sat + (lane & 15)] : 0.0f;
-#pragma unroll
-          for (int i = 0; i < ITER; ++i) {
-            const int p = i * 32 + lane;
-            x[gi][i] = make_uint2(0, 0);
-            if (p < 16 * chunks && ((pl[gi].rows >> ((p * recip) >> 16)) & 1))
-              x[gi][i] = *reinterpret_cast<const uint2 *>(kv + pl[gi].at + p * 8);
+      Place pl[2];       // of the tile whose copies are under way
+      uint32_t rows[4];  // visible ones of the four pieces in the ring
+      uint32_t fetched[4] = {0, 0, 0, 0};
+      auto fetch = [&](int q) {  // piece q: keys (0, 1) or values (2, 3), 16 tokens q % 2
+        const Place &p = pl[q % 2];
+        rows[q] = p.rows;
+        ++fetched[q];
+        if (lane == 0) {
+          uint64_t *bar = &bars->raw[w2][q];
+          if (p.rows) {
+            const uint8_t *kv = (q < 2 ? a.c.k : a.c.v) + p.at;
+            const float *sc = (q < 2 ? a.c.ks : a.c.vs) + p.sat;
+            mbar_arrive_expect_tx(bar, 16 * D + 64);
+            bulk_load(raw + q * S::RAW, kv, 16 * D, bar);
+            bulk_load(raw + q * S::RAW + 16 * DP, sc, 64, bar);
+          } else {
+            mbar_arrive(bar);
           }
         }
       };
-      auto store = [&](int u, const uint2 (&x)[2][ITER], const float (&s)[2]) -> bool {
-        bool fine = true;
-        if (u >= S::SLOTS) fine = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
-        if (!__all_sync(FULL, fine)) return false;
-        uint8_t *st = slot_of(u);
+      auto places = [&](int j) {
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
-          const uint32_t h = (uint32_t)__half_as_ushort(__float2half_rn(s[gi]));
-#pragma unroll
-          for (int i = 0; i < ITER; ++i) {
-            const int p = i * 32 + lane;
-            const uint32_t one = __shfl_sync(FULL, h, ((p * recip) >> 16) & 15);
-            if (p < 16 * chunks)
-              *reinterpret_cast<uint4 *>(st + dst_of(gi, p)) = pr_convert(x[gi][i], one | (one << 16));
-          }
+          pl[gi] = place(j, gi, page[gi]);
+          page[gi] = page_of(j + 1, gi);
         }
-        arrive(u);
-        return true;
       };
-      if (n > 0) fetch(0, raw[0], sc[0]);
-      for (int u = 0; u < n && ok; u += 2) {  // n is even
-        fetch(u + 1, raw[1], sc[1]);
-        ok = store(u, raw[0], sc[0]);
-        if (!ok) break;
-        if (u + 2 < n) fetch(u + 2, raw[0], sc[0]);
-        ok = store(u + 1, raw[1], sc[1]);
+      if (steps > 0) {
+        places(0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) fetch(q);
       }
+      int j = 0;
+      for (; j < steps && ok; ++j) {
+        if (j + 1 < steps) places(j + 1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int u = 2 * j + q / 2;
+          bool fine = true;
+          if (q % 2 == 0 && u >= S::SLOTS) fine = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
+          fine = fine && pr_wait(bars, &bars->raw[w2][q], j & 1);
+          ok = __all_sync(FULL, fine);
+          if (!ok) break;
+          uint8_t *st = slot_of(u);
+          const uint8_t *from = raw + q * S::RAW;
+          const float sc = *reinterpret_cast<const float *>(from + 16 * DP + (lane & 15) * 4);
+          uint32_t one = (uint32_t)__half_as_ushort(__float2half_rn(sc));
+          one |= one << 16;
+          const bool whole = rows[q] == 0xffffu;
+#pragma unroll
+          for (int i = 0; i < ITER; ++i) {
+            const int p = i * 32 + lane, r = (int)((p * recip) >> 16) & 15;
+            const uint32_t s2 = __shfl_sync(FULL, one, r);
+            if (p < 16 * chunks) {
+              uint4 x = pr_convert(*reinterpret_cast<const uint2 *>(from + p * 8), s2);
+              if (!whole && !((rows[q] >> r) & 1)) x = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4 *>(st + dst_of(q % 2, p)) = x;
+            }
+          }
+          __syncwarp();  // the piece has been read
+          if (j + 1 < steps) fetch(q);
+          if (q % 2) arrive(u);
+        }
+      }
+      if (!ok && lane == 0)  // copies under way land before the block ends
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (!mbar_wait(&bars->raw[w2][q], (fetched[q] - 1) & 1, DRAIN_NS)) bars->undrained = 1;
     }
     if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
   } else {
@@ -638,8 +733,8 @@ template <int DP, bool E4M3>
 static cudaError_t launch_prompt_t(const PrArgs &A, int64_t blocks, cudaStream_t s) {
   static SmemOptIn opt_in;
   auto kern = k_attn_prompt<DP, E4M3>;
-  if (cudaError_t e = opt_in(kern, PrShape<DP>::SMEM)) return e;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PR_THREADS), PrShape<DP>::SMEM, s, A);
+  if (cudaError_t e = opt_in(kern, PrShape<DP, E4M3>::SMEM)) return e;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PR_THREADS), PrShape<DP, E4M3>::SMEM, s, A);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
