@@ -71,7 +71,7 @@ struct PrItem {
 };
 
 struct PrBars {
-  uint64_t full[8], empty[8], raw[4][4], turn[2];
+  uint64_t full[8], empty[8], raw[4][4];
   uint64_t q_ready;
   uint64_t s_ready[2], p_ready[2][2], o_done[2], drain[2];
   uint32_t tmem_base;
@@ -80,7 +80,6 @@ struct PrBars {
 };
 
 __device__ __forceinline__ bool pr_wait(PrBars *b, uint64_t *bar, uint32_t parity) {
-  if (*(volatile int32_t *)&b->timeout) return false;
   // no suspend-time hint: these waits are short and follow one another in a chain
   const uint32_t at = smem_addr(bar);
   uint64_t t0 = 0;
@@ -97,7 +96,7 @@ __device__ __forceinline__ bool pr_wait(PrBars *b, uint64_t *bar, uint32_t parit
     if (i % 64 == 63) {
       const uint64_t t = global_ns();
       if (t0 == 0) t0 = t;
-      else if (t - t0 > 2000000000ull) break;
+      else if (t - t0 > 2000000000ull || *(volatile int32_t *)&b->timeout) break;
     }
   }
   b->timeout = 1;
@@ -280,7 +279,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       mbar_init(&bars->p_ready[i][1], 4);
       mbar_init(&bars->o_done[i], 1);
       mbar_init(&bars->drain[i], 1);
-      mbar_init(&bars->turn[i], 4);
     }
     for (int i = 0; i < 16; ++i) mbar_init(&bars->raw[i / 4][i % 4], 1);
     bars->timeout = bars->undrained = 0;
@@ -315,13 +313,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       uint8_t *qs = base + w * S::TILE;
       const int used = it.cnt[w] * A.group;
       const uint16_t *src = a.q + (it.row0 + (int64_t)w * A.R) * a.ldq + (int64_t)it.head * A.group * D;
+      const uint32_t by_chunks = 65536u / chunks + 1, by_group = 65536u / A.group + 1;  // exact below 2048
       for (int p = threadIdx.x % 128; p < PR_T * chunks; p += 128) {
-        const int rr = p / chunks, c = p - rr * chunks, tok = rr / A.group;
-        const uint16_t *from = src + (int64_t)tok * a.ldq + (int64_t)(rr - tok * A.group) * D + c * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (rr < used) v = *reinterpret_cast<const uint4 *>(from);
-        *reinterpret_cast<uint4 *>(qs + (c / 8) * (PR_T * 128) + swz128(rr, c % 8)) = v;
+        const int rr = (int)((p * by_chunks) >> 16), c = p - rr * chunks, i = (int)((rr * by_group) >> 16);
+        const bool in = rr < used;
+        const uint16_t *from = in ? src + (int64_t)i * a.ldq + (int64_t)(rr - i * A.group) * D + c * 8 : a.q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_addr(qs) + (c / 8) * (PR_T * 128) + swz128(rr, c % 8)),
+                     "l"(from), "r"(in ? 16 : 0)
+                     : "memory");
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_ready);
@@ -335,7 +337,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       float m = -INFINITY, l = 0.0f;
       bool first = true, ok = true;
       uint32_t phase = 0;
-      int turns = 0;  // steps in which both tiles took part
       const uint32_t ts = tmem_addr(tmem, q * 32, w * 128), to = tmem_addr(tmem, q * 32, 256 + w * 128);
       for (int j = 0; j < steps; ++j) {
         const int t = pr_tile(it, j), j0 = t * PR_T;
@@ -345,12 +346,27 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         phase ^= 1;
         tc_fence_after();
         uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, v[c]);
+        tmem_ld32(ts, v[0]);
+        tmem_ld32(ts + 32, v[1]);
         tmem_wait_ld();
+        tmem_ld32(ts + 64, v[2]);
+        tmem_ld32(ts + 96, v[3]);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto most = [&](int c0) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+#pragma unroll
+            for (int c = c0; c < c0 + 2; ++c)
+              top[c] = fmaxf(fmaxf(top[c], __uint_as_float(v[c][i])), __uint_as_float(v[c][i + 1]));
+        };
         const bool all = j0 + PR_T - 1 <= p_min &&
                          (!a.window || j0 > p_max - a.window || j0 + PR_T <= a.sinks);
-        if (!all) {
+        if (all) {
+          most(0);
+          tmem_wait_ld();
+          most(2);
+        } else {
+          tmem_wait_ld();
           asm volatile("");  // a branch, not selects in every tile
           const int hi = valid ? min(p - j0, PR_T) : -1;
           const int lo = (int)min(max(lo64 - j0, (int64_t)-1), (int64_t)PR_T + 1);
@@ -362,12 +378,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
               const int x = c * 32 + i;
               if (x > hi || (x < lo && x >= sk)) v[c][i] = 0xff800000u;
             }
+          most(0);
+          most(2);
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(v[c][i]));
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
         const bool up = mx > m + PR_SLACK || (m == -INFINITY && mx > m);
         if (__any_sync(FULL, up)) {
@@ -390,13 +403,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         }
         first = false;
         const float z = m == -INFINITY ? 0.0f : m;
-        // the two tiles take turns: side by side they would wait for the same units, and
-        // then for the tensor cores, both at once
-        const bool both = pr_active(it, 1 - w, t);
-        if (both && (w == 1 || turns > 0)) {
-          ok = __all_sync(FULL, pr_wait(bars, &bars->turn[w], (turns - 1 + w) & 1));
-          if (!ok) break;
-        }
         const uint64_t cc = pk2(c2, c2), zz = pk2(-z, -z);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -419,10 +425,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
             pk[i] = *reinterpret_cast<const uint32_t *>(&two);
           }
           tmem_st32(ts + h * 32, pk);
-          if (h == 1 && both) {
-            if (lane == 0) mbar_arrive(&bars->turn[1 - w]);
-            ++turns;
-          }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -432,13 +434,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         l += sa.x + sa.y;
       }
       // output
-      uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R + tok) * a.ldo +
-                      ((int64_t)it.head * A.group + (r - tok * A.group)) * D;
       bool finite = true;
       if (it.last[w] >= 0 && ok) ok = __all_sync(FULL, pr_wait(bars, &bars->o_done[w], 0));
       if (ok) {
         tc_fence_after();
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a row that sees nothing: zeros
+        // through shared memory (Q has been read), so that rows are written whole
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
           if (c * 32 >= D) break;
@@ -447,21 +448,30 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
             tmem_ld32(to + c * 32, o);
             tmem_wait_ld();
           }
-          if (!valid) continue;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (c * 32 + i * 8 >= D) break;
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = inv == 0.0f ? 0.0f : __uint_as_float(o[i * 8 + 2 * e]) * inv;
               const float y = inv == 0.0f ? 0.0f : __uint_as_float(o[i * 8 + 2 * e + 1]) * inv;
-              finite &= x - x == 0.0f && y - y == 0.0f;
+              if (valid && c * 32 + i * 8 < D) finite &= x - x == 0.0f && y - y == 0.0f;
               const __half2 two = __floats2half2_rn(x, y);
               h[e] = *reinterpret_cast<const uint32_t *>(&two);
             }
-            *reinterpret_cast<uint4 *>(out + c * 32 + i * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+            const int cc = c * 4 + i;
+            *reinterpret_cast<uint4 *>(qs + (cc / 8) * (PR_T * 128) + swz128(r, cc % 8)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
           }
+        }
+        __syncwarp();
+        uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R) * a.ldo + (int64_t)it.head * A.group * D;
+        for (int p = lane; p < 32 * chunks; p += 32) {
+          const int r0 = (int)((p * by_chunks) >> 16), c = p - r0 * chunks, rr = q * 32 + r0;
+          if (rr >= used) break;
+          const int i = (int)((rr * by_group) >> 16);
+          *reinterpret_cast<uint4 *>(out + (int64_t)i * a.ldo + (int64_t)(rr - i * A.group) * D + c * 8) =
+              *reinterpret_cast<const uint4 *>(qs + (c / 8) * (PR_T * 128) + swz128(rr, c % 8));
         }
       }
       if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
@@ -610,15 +620,29 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
           const float sc = *reinterpret_cast<const float *>(from + 16 * DP + (lane & 15) * 4);
           uint32_t one = (uint32_t)__half_as_ushort(__float2half_rn(sc));
           one |= one << 16;
-          const bool whole = rows[q] == 0xffffu;
+          if (D == DP && rows[q] == 0xffffu) {
+            // all loads, then all stores: nothing waits for a piece by itself
+            constexpr int C = DP / 8;  // chunks of a row
+            uint2 x[ITER];
 #pragma unroll
-          for (int i = 0; i < ITER; ++i) {
-            const int p = i * 32 + lane, r = (int)((p * recip) >> 16) & 15;
-            const uint32_t s2 = __shfl_sync(FULL, one, r);
-            if (p < 16 * chunks) {
-              uint4 x = pr_convert(*reinterpret_cast<const uint2 *>(from + p * 8), s2);
-              if (!whole && !((rows[q] >> r) & 1)) x = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4 *>(st + dst_of(q % 2, p)) = x;
+            for (int i = 0; i < ITER; ++i) x[i] = *reinterpret_cast<const uint2 *>(from + (i * 32 + lane) * 8);
+            uint8_t *to = st + ((lane % C) / 8) * (PR_T * 128) + (q % 2) * 2048;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+              const int r = i * (32 / C) + lane / C;
+              *reinterpret_cast<uint4 *>(to + (w2 * 32 * 128) + swz128(r, lane % 8)) =
+                  pr_convert(x[i], __shfl_sync(FULL, one, r));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+              const int p = i * 32 + lane, r = (int)((p * recip) >> 16) & 15;
+              const uint32_t s2 = __shfl_sync(FULL, one, r);
+              if (p < 16 * chunks) {
+                uint4 x = pr_convert(*reinterpret_cast<const uint2 *>(from + p * 8), s2);
+                if (!((rows[q] >> r) & 1)) x = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(st + dst_of(q % 2, p)) = x;
+              }
             }
           }
           __syncwarp();  // the piece has been read
@@ -645,7 +669,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       const uint32_t s0 = __shfl_sync(FULL, smem_addr(base), 0);
       const uint32_t ts = __shfl_sync(FULL, tmem, 0) + w * 128, to = ts + 256;
       const uint64_t qa = smem_desc_k_sw128(s0 + w * S::TILE);
-      const uint64_t ring = smem_desc_k_sw128(s0 + 2 * S::TILE);
+      const uint64_t ring_k = smem_desc_k_sw128(s0 + 2 * S::TILE);
       const uint64_t ring_mn = smem_desc_mn_sw128(s0 + 2 * S::TILE, PR_T * 128);
       const int last = __shfl_sync(FULL, it.last[w], 0), first = __shfl_sync(FULL, it.first[w], 0);
       const int sink = __shfl_sync(FULL, it.sink[w], 0);
@@ -655,17 +679,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         return t <= last && (t >= first || t < sink);
       };
       auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, pr_wait(bars, bar, parity)); };
-      // keys of step j: slot and phase of tile 2 j, values: of 2 j + 1
-      int slot = 0;
-      uint32_t phase = 0, p_phase = 0, more = 0;
-      auto next = [&]() {
-        if (++slot == S::SLOTS) {
-          slot = 0;
-          phase ^= 1;
+      struct Ring {
+        int slot;
+        uint32_t phase;
+        __device__ void next() {
+          if (++slot == S::SLOTS) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       };
-      auto qk = [&]() {
-        const uint64_t kb = ring + (uint64_t)(slot * (S::TILE >> 4));
+      Ring ring = {0, 0};
+      uint32_t p_phase = 0, more = 0;
+      auto qk = [&](int slot) {
+        const uint64_t kb = ring_k + (uint64_t)(slot * (S::TILE >> 4));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           if (k >= ks) break;
@@ -674,38 +701,43 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         }
         tc_commit_if(on, &bars->s_ready[w]);
       };
-      bool ok = ready(&bars->q_ready, 0);
-      for (int j = 0; j <= n && ok; ++j) {
-        if (j > 0) {  // the values of step j - 1
-          ok = ready(&bars->full[slot], phase);
-          if (!ok) break;
-          if (active(j - 1)) {
-            const uint64_t vb = ring_mn + (uint64_t)(slot * (S::TILE >> 4));
+      bool ok = ready(&bars->q_ready, 0) && ready(&bars->full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        if (active(0)) qk(0);
+        tc_commit_if(on, &bars->empty[0]);
+        ring.next();
+      }
+      // Both tiles that a step needs are waited for ahead of the weights, and nothing
+      // stands between the last weights and the next scores: this chain, with the
+      // softmax, is what a step takes.
+      for (int j = 0; j < n && ok; ++j) {
+        const int sv = ring.slot;  // the values of step j, then the keys of step j + 1
+        ok = ready(&bars->full[sv], ring.phase);
+        ring.next();
+        const int sk = ring.slot;
+        const bool go = active(j), go_on = j + 1 < n && active(j + 1);
+        if (j + 1 < n) ok = ok && ready(&bars->full[sk], ring.phase);
+        const uint64_t vb = ring_mn + (uint64_t)(sv * (S::TILE >> 4));
+        if (go) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && ready(&bars->p_ready[w][h], p_phase);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                mma_f16_ts_if(on, to, ts + (h * 4 + k) * 8, vb + (uint64_t)((h * 4 + k) * (2048 >> 4)), id_pv, more);
-                more = 1;
-              }
-            }
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && ready(&bars->p_ready[w][h], p_phase);
             if (!ok) break;
-            p_phase ^= 1;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              mma_f16_ts_if(on, to, ts + (h * 4 + k) * 8, vb + (uint64_t)((h * 4 + k) * (2048 >> 4)), id_pv, more);
+              more = 1;
+            }
           }
-          tc_commit_if(on, j == n ? &bars->o_done[w] : &bars->empty[slot]);
-          next();
+          p_phase ^= 1;
         }
-        if (j < n) {  // the keys of step j
-          ok = ready(&bars->full[slot], phase);
-          if (!ok) break;
-          tc_fence_after();
-          if (active(j)) qk();
-          tc_commit_if(on, &bars->empty[slot]);
-          next();
-        }
+        if (!ok) break;
+        if (go_on) qk(sk);
+        tc_commit_if(on, j + 1 == n ? &bars->o_done[w] : &bars->empty[sv]);
+        if (j + 1 < n) tc_commit_if(on, &bars->empty[sk]);
+        ring.next();
       }
       // every MMA has completed before TMEM is released
       tc_commit_if(on, &bars->drain[w]);
