@@ -38,11 +38,9 @@ namespace bwta {
 constexpr int PR_T = 128;           // rows of a tile, tokens of a key tile
 constexpr int PR_THREADS = 512;
 constexpr int PR_LAG = 2;           // key or value tiles whose copies are in flight
-constexpr int PR_POLY = 4;          // one pair of weights in so many goes to the FMA units
+constexpr int PR_HALF = 64;         // keys of one product (scores and weights)
+constexpr int PR_POLY = 8;          // one pair of weights in so many goes to the FMA units
 constexpr float PR_SLACK = 8.0f;    // how far scores may pass the reference (log2)
-// Registers by role: 2 x 184 + 104 + 40 = 512 = the block's 65536 / 128.
-constexpr int PR_REG_SOFTMAX = 184, PR_REG_LOAD = 104, PR_REG_MMA = 40;
-
 template <int DP, bool E4M3>
 struct PrShape {
   static constexpr int NH = DP / 64;                  // halves of 64 columns
@@ -73,7 +71,7 @@ struct PrItem {
 struct PrBars {
   uint64_t full[8], empty[8], raw[4][4];
   uint64_t q_ready;
-  uint64_t s_ready[2], p_ready[2][2], o_done[2], drain[2];
+  uint64_t s_ready[2][2], p_ready[2][2], pv_done[2], o_done[2], drain[2];
   uint32_t tmem_base;
   int32_t timeout, undrained;
   PrItem item;
@@ -108,15 +106,6 @@ __device__ __forceinline__ int pr_tile(const PrItem &it, int j) {
 }
 __device__ __forceinline__ bool pr_active(const PrItem &it, int a, int t) {
   return t <= it.last[a] && (t >= it.first[a] || t < it.sink[a]);
-}
-
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Block -> sequence, key head and pair of tiles. The pairs of a (sequence, head)
@@ -274,7 +263,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     }
     mbar_init(&bars->q_ready, 8);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_ready[i], 1);
+      mbar_init(&bars->s_ready[i][0], 1);
+      mbar_init(&bars->s_ready[i][1], 1);
+      mbar_init(&bars->pv_done[i], 1);
       mbar_init(&bars->p_ready[i][0], 4);
       mbar_init(&bars->p_ready[i][1], 4);
       mbar_init(&bars->o_done[i], 1);
@@ -305,7 +296,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
 
   if (warp >= 8) {
     // ------------------------------------------------ softmax and output
-    regs_inc<PR_REG_SOFTMAX>();
     const int w = warp / 4 - 2, q = warp % 4, r = q * 32 + lane;
     if (it.live) {
       const int chunks = D / 8;
@@ -335,82 +325,74 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       const int p_min = it.pmin[w], p_max = it.pmin[w] + it.cnt[w] - 1;
       const float c2 = a.scale * 1.44269504088896340736f;
       float m = -INFINITY, l = 0.0f;
-      bool first = true, ok = true;
-      uint32_t phase = 0;
+      bool ok = true;
+      uint32_t halves = 0;  // of key tiles, so far
       const uint32_t ts = tmem_addr(tmem, q * 32, w * 128), to = tmem_addr(tmem, q * 32, 256 + w * 128);
-      for (int j = 0; j < steps; ++j) {
-        const int t = pr_tile(it, j), j0 = t * PR_T;
+      const uint64_t cc = pk2(c2, c2);
+      for (int j = 0; j < steps && ok; ++j) {
+        const int t = pr_tile(it, j);
         if (!pr_active(it, w, t)) continue;
-        ok = __all_sync(FULL, pr_wait(bars, &bars->s_ready[w], phase));
-        if (!ok) break;
-        phase ^= 1;
-        tc_fence_after();
-        uint32_t v[4][32];
-        tmem_ld32(ts, v[0]);
-        tmem_ld32(ts + 32, v[1]);
-        tmem_wait_ld();
-        tmem_ld32(ts + 64, v[2]);
-        tmem_ld32(ts + 96, v[3]);
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto most = [&](int c0) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-#pragma unroll
-            for (int c = c0; c < c0 + 2; ++c)
-              top[c] = fmaxf(fmaxf(top[c], __uint_as_float(v[c][i])), __uint_as_float(v[c][i + 1]));
-        };
-        const bool all = j0 + PR_T - 1 <= p_min &&
-                         (!a.window || j0 > p_max - a.window || j0 + PR_T <= a.sinks);
-        if (all) {
-          most(0);
+        for (int h = 0; h < 2; ++h, ++halves) {
+          const int j0 = t * PR_T + h * PR_HALF;
+          const bool all = j0 + PR_HALF - 1 <= p_min &&
+                           (!a.window || j0 > p_max - a.window || j0 + PR_HALF <= a.sinks);
+          ok = __all_sync(FULL, pr_wait(bars, &bars->s_ready[w][h], (halves >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t v[2][32];
+          tmem_ld32(ts + h * PR_HALF, v[0]);
+          tmem_ld32(ts + h * PR_HALF + 32, v[1]);
           tmem_wait_ld();
-          most(2);
-        } else {
-          tmem_wait_ld();
-          asm volatile("");  // a branch, not selects in every tile
-          const int hi = valid ? min(p - j0, PR_T) : -1;
-          const int lo = (int)min(max(lo64 - j0, (int64_t)-1), (int64_t)PR_T + 1);
-          const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_T + 1);
+          if (!all) {
+            asm volatile("");  // a branch, not selects in every tile
+            const int hi = valid ? min(p - j0, PR_T) : -1;
+            const int lo = (int)min(max(lo64 - j0, (int64_t)-1), (int64_t)PR_T + 1);
+            const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_T + 1);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int x = c * 32 + i;
-              if (x > hi || (x < lo && x >= sk)) v[c][i] = 0xff800000u;
-            }
-          most(0);
-          most(2);
-        }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
-        const bool up = mx > m + PR_SLACK || (m == -INFINITY && mx > m);
-        if (__any_sync(FULL, up)) {
-          const float mn = up ? mx : m;
-          // nothing seen so far: the sums are zero and the factor does not matter
-          const float f = m == -INFINITY ? 0.0f : pr_exp2(m - mn);
-          m = mn;
-          l *= f;
-          if (!first) {  // S being ready, the MMAs before it are complete: O holds still
+              for (int i = 0; i < 32; ++i) {
+                const int x = c * 32 + i;
+                if (x > hi || (x < lo && x >= sk)) v[c][i] = 0xff800000u;
+              }
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(to + c * 16, o);
-              tmem_wait_ld();
+          for (int i = 0; i < 32; i += 4)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(to + c * 16, o);
+            for (int c = 0; c < 4; ++c)
+              top[c] = fmaxf(fmaxf(top[c], __uint_as_float(v[c / 2][i + (c % 2) * 2])),
+                             __uint_as_float(v[c / 2][i + (c % 2) * 2 + 1]));
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
+          const bool up = mx > m + PR_SLACK || (m == -INFINITY && mx > m);
+          if (__any_sync(FULL, up)) {
+            const float mn = up ? mx : m;
+            // nothing seen so far: the sums are zero and the factor does not matter
+            const float f = m == -INFINITY ? 0.0f : pr_exp2(m - mn);
+            m = mn;
+            l *= f;
+            if (halves > 0) {  // the product before this one is complete: O holds still
+              ok = __all_sync(FULL, pr_wait(bars, &bars->pv_done[w], (halves - 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < DP / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(to + c * 16, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(to + c * 16, o);
+              }
             }
           }
-        }
-        first = false;
-        const float z = m == -INFINITY ? 0.0f : m;
-        const uint64_t cc = pk2(c2, c2), zz = pk2(-z, -z);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          const float z = m == -INFINITY ? 0.0f : m;
+          const uint64_t zz = pk2(-z, -z);
+          uint64_t sum[2] = {0, 0};
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int c = h * 2 + i / 16, e = (i % 16) * 2;
+            const int c = i / 16, e = (i % 16) * 2;
             const uint64_t x = fma2(pk2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), cc, zz);
             float2 y;
             if (i % PR_POLY == PR_POLY - 1) {
@@ -424,14 +406,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
             const __half2 two = __floats2half2_rn(y.x, y.y);
             pk[i] = *reinterpret_cast<const uint32_t *>(&two);
           }
-          tmem_st32(ts + h * 32, pk);
+          tmem_st32(ts + h * PR_HALF, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->p_ready[w][h]);
+          const float2 sa = up2(add2(sum[0], sum[1]));
+          l += sa.x + sa.y;
         }
-        const float2 sa = up2(add2(sum[0], sum[1]));
-        l += sa.x + sa.y;
       }
       // output
       bool finite = true;
@@ -478,7 +460,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ keys and values
-    regs_dec<PR_REG_LOAD>();
     constexpr int ITER = DP / 16;  // 16-byte chunks of fp16 a lane holds of 16 rows
     const int chunks = D / 8, n = 2 * steps;
     const uint32_t recip = 65536u / chunks + 1;  // p / chunks = (p * recip) >> 16 for p < 256
@@ -658,12 +639,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
   } else {
     // ------------------------------------------------ MMA issue
-    regs_dec<PR_REG_MMA>();
     // warp w issues the products of tile w, all lanes in step
     if (warp < 2 && steps > 0) {
       const int w = warp, n = __shfl_sync(FULL, steps, 0);
       const uint32_t on = lane == 0;
-      const uint32_t id_qk = idesc_f16_f32(PR_T, PR_T);
+      const uint32_t id_qk = idesc_f16_f32(PR_T, PR_HALF);
       const uint32_t id_pv = idesc_f16_f32(PR_T, (D + 15) / 16 * 16) | IDESC_B_MN;
       const int ks = (D + 15) / 16;
       const uint32_t s0 = __shfl_sync(FULL, smem_addr(base), 0);
@@ -691,26 +671,29 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       };
       Ring ring = {0, 0};
       uint32_t p_phase = 0, more = 0;
-      auto qk = [&](int slot) {
-        const uint64_t kb = ring_k + (uint64_t)(slot * (S::TILE >> 4));
+      auto qk = [&](int slot, int h) {
+        const uint64_t kb = ring_k + (uint64_t)((slot * S::TILE + h * PR_HALF * 128) >> 4);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           if (k >= ks) break;
           const uint32_t off = ((k / 4) * (PR_T * 128) + (k % 4) * 32) >> 4;
-          mma_f16_ss_if(on, ts, qa + off, kb + off, id_qk, k > 0);
+          mma_f16_ss_if(on, ts + h * PR_HALF, qa + off, kb + off, id_qk, k > 0);
         }
-        tc_commit_if(on, &bars->s_ready[w]);
+        tc_commit_if(on, &bars->s_ready[w][h]);
       };
       bool ok = ready(&bars->q_ready, 0) && ready(&bars->full[0], 0);
       if (ok) {
         tc_fence_after();
-        if (active(0)) qk(0);
+        if (active(0)) {
+          qk(0, 0);
+          qk(0, 1);
+        }
         tc_commit_if(on, &bars->empty[0]);
         ring.next();
       }
-      // Both tiles that a step needs are waited for ahead of the weights, and nothing
-      // stands between the last weights and the next scores: this chain, with the
-      // softmax, is what a step takes.
+      // Both tiles of keys and values that a step needs are waited for ahead of the
+      // weights, and nothing stands between the weights of a half and the next scores
+      // in its place.
       for (int j = 0; j < n && ok; ++j) {
         const int sv = ring.slot;  // the values of step j, then the keys of step j + 1
         ok = ready(&bars->full[sv], ring.phase);
@@ -719,22 +702,25 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         const bool go = active(j), go_on = j + 1 < n && active(j + 1);
         if (j + 1 < n) ok = ok && ready(&bars->full[sk], ring.phase);
         const uint64_t vb = ring_mn + (uint64_t)(sv * (S::TILE >> 4));
-        if (go) {
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          if (go) {
             ok = ok && ready(&bars->p_ready[w][h], p_phase);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              mma_f16_ts_if(on, to, ts + (h * 4 + k) * 8, vb + (uint64_t)((h * 4 + k) * (2048 >> 4)), id_pv, more);
+              mma_f16_ts_if(on, to, ts + h * PR_HALF + k * 8, vb + (uint64_t)((h * 4 + k) * (2048 >> 4)), id_pv, more);
               more = 1;
             }
+            tc_commit_if(on, &bars->pv_done[w]);
           }
-          p_phase ^= 1;
+          if (go_on) qk(sk, h);
         }
         if (!ok) break;
-        if (go_on) qk(sk);
+        if (go) p_phase ^= 1;
         tc_commit_if(on, j + 1 == n ? &bars->o_done[w] : &bars->empty[sv]);
         if (j + 1 < n) tc_commit_if(on, &bars->empty[sk]);
         ring.next();
