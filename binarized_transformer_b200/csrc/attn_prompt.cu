@@ -36,10 +36,19 @@
 namespace bwta {
 
 constexpr int PR_T = 128;           // rows of a tile, tokens of a key tile
-constexpr int PR_THREADS = 512;
+// E4M3 takes twice the warps for the keys and values: they convert them.
+template <bool E4M3>
+struct PrWarps {
+  static constexpr int LOAD = E4M3 ? 8 : 4;
+  static constexpr int SOFTMAX0 = 4 + LOAD;  // the first softmax warp
+  static constexpr int THREADS = (4 + LOAD + 8) * 32;
+  // Registers by role; launched with 128 (96) a thread, so 4 x 128 (5 x 96) in all.
+  static constexpr int REG_MMA = E4M3 ? 56 : 104, REG_LOAD = E4M3 ? 72 : 104;
+  static constexpr int REG_SOFTMAX = E4M3 ? 136 : 152;
+  static_assert(REG_MMA + LOAD / 4 * REG_LOAD + 2 * REG_SOFTMAX <= (E4M3 ? 5 * 96 : 4 * 128), "registers");
+};
 constexpr int PR_LAG = 2;           // key or value tiles whose copies are in flight
 constexpr int PR_HALF = 64;         // keys of one product (scores and weights)
-constexpr int PR_POLY = 8;          // one pair of weights in so many goes to the FMA units
 constexpr float PR_SLACK = 8.0f;    // how far scores may pass the reference (log2)
 template <int DP, bool E4M3>
 struct PrShape {
@@ -69,7 +78,7 @@ struct PrItem {
 };
 
 struct PrBars {
-  uint64_t full[8], empty[8], raw[4][4];
+  uint64_t full[8], empty[8], raw[8][2];
   uint64_t q_ready;
   uint64_t s_ready[2][2], p_ready[2][2], pv_done[2], o_done[2], drain[2];
   uint32_t tmem_base;
@@ -106,6 +115,15 @@ __device__ __forceinline__ int pr_tile(const PrItem &it, int j) {
 }
 __device__ __forceinline__ bool pr_active(const PrItem &it, int a, int t) {
   return t <= it.last[a] && (t >= it.first[a] || t < it.sink[a]);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Block -> sequence, key head and pair of tiles. The pairs of a (sequence, head)
@@ -192,6 +210,9 @@ __device__ __forceinline__ uint4 pr_convert(uint2 b, uint32_t scale2) {
   return make_uint4(two(b.x & 0xffffu), two(b.x >> 16), two(b.y & 0xffffu), two(b.y >> 16));
 }
 
+// The lowest n bits.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+
 __device__ __forceinline__ float pr_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -220,33 +241,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 2^x for two numbers on the FMA units, for a part of a row's weights: the unit that
-// has the exponential takes 16 a clock, as long for a tile as the tensor cores.
-// x = n + f, n the nearest integer; 2^f on [-1/2, 1/2] by a polynomial of degree 5
-// (equal-ripple fit of the relative error, 7.5e-8), n added to the exponent. Below
-// -126 it stays 2^-126, nothing to fp16; a NaN ends as an infinite weight in fp16.
-__device__ __forceinline__ float2 pr_exp2_poly(uint64_t x) {
-  float2 v = up2(x);
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.x));
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.y));
-  const uint64_t c = pk2(v.x, v.y), magic = pk2(12582912.0f, 12582912.0f);
-  const uint64_t r = add2(c, magic);                                     // 1.5 * 2^23 + n
-  const uint64_t nf = add2(r, pk2(-12582912.0f, -12582912.0f));
-  const uint64_t f = fma2(nf, pk2(-1.0f, -1.0f), c);
-  uint64_t p = pk2(0.0013276472f, 0.0013276472f);
-  p = fma2(p, f, pk2(0.0096755413f, 0.0096755413f));
-  p = fma2(p, f, pk2(0.0555071327f, 0.0555071327f));
-  p = fma2(p, f, pk2(0.2402211972f, 0.2402211972f));
-  p = fma2(p, f, pk2(0.6931469671f, 0.6931469671f));
-  p = fma2(p, f, pk2(1.0000000717f, 1.0000000717f));
-  const float2 n = up2(r), y = up2(p);
-  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(n.x) << 23)),
-                     __int_as_float(__float_as_int(y.y) + (__float_as_int(n.y) << 23)));
-}
-
 template <int DP, bool E4M3>
-__global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
+__global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const PrArgs A) {
   using S = PrShape<DP, E4M3>;
+  using W = PrWarps<E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
-      mbar_init(&bars->full[i], 4);
+      mbar_init(&bars->full[i], W::LOAD);
       mbar_init(&bars->empty[i], 2);
     }
     mbar_init(&bars->q_ready, 8);
@@ -271,12 +269,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       mbar_init(&bars->o_done[i], 1);
       mbar_init(&bars->drain[i], 1);
     }
-    for (int i = 0; i < 16; ++i) mbar_init(&bars->raw[i / 4][i % 4], 1);
+    for (int i = 0; i < 16; ++i) mbar_init(&bars->raw[i / 2][i % 2], 1);
     bars->timeout = bars->undrained = 0;
     mbar_fence_init();
   }
   if (D % 16 != 0) {  // the products read 8 columns past D, which are never written: zero once
-    for (int i = threadIdx.x * 16; i < (2 + S::SLOTS) * S::TILE; i += PR_THREADS * 16)
+    for (int i = threadIdx.x * 16; i < (2 + S::SLOTS) * S::TILE; i += W::THREADS * 16)
       *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -294,9 +292,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
   // TMEM columns: S0 0, S1 128, O0 256, O1 384 (P of a tile: the first 64 of its S)
   const int steps = it.live ? it.steps : 0;
 
-  if (warp >= 8) {
+  if (warp >= W::SOFTMAX0) {
     // ------------------------------------------------ softmax and output
-    const int w = warp / 4 - 2, q = warp % 4, r = q * 32 + lane;
+    regs_inc<W::REG_SOFTMAX>();
+    const int w = (warp - W::SOFTMAX0) / 4, q = warp % 4, r = q * 32 + lane;
     if (it.live) {
       const int chunks = D / 8;
       // Q rows of this tile, into the layout of the keys
@@ -304,6 +303,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       const int used = it.cnt[w] * A.group;
       const uint16_t *src = a.q + (it.row0 + (int64_t)w * A.R) * a.ldq + (int64_t)it.head * A.group * D;
       const uint32_t by_chunks = 65536u / chunks + 1, by_group = 65536u / A.group + 1;  // exact below 2048
+#pragma unroll 1
       for (int p = threadIdx.x % 128; p < PR_T * chunks; p += 128) {
         const int rr = (int)((p * by_chunks) >> 16), c = p - rr * chunks, i = (int)((rr * by_group) >> 16);
         const bool in = rr < used;
@@ -344,17 +344,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
           tmem_ld32(ts + h * PR_HALF + 32, v[1]);
           tmem_wait_ld();
           if (!all) {
-            asm volatile("");  // a branch, not selects in every tile
-            const int hi = valid ? min(p - j0, PR_T) : -1;
-            const int lo = (int)min(max(lo64 - j0, (int64_t)-1), (int64_t)PR_T + 1);
-            const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_T + 1);
+            const int hi = valid ? p - j0 : -1;
+            const int lo = (int)min(max(lo64 - j0, (int64_t)0), (int64_t)PR_HALF);
+            const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_HALF);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t see = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int x = c * 32 + i;
-                if (x > hi || (x < lo && x >= sk)) v[c][i] = 0xff800000u;
-              }
+              for (int i = 0; i < 32; ++i)
+                if (!((see >> i) & 1)) v[c][i] = 0xff800000u;
+            }
           }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -393,15 +392,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int c = i / 16, e = (i % 16) * 2;
-            const uint64_t x = fma2(pk2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), cc, zz);
-            float2 y;
-            if (i % PR_POLY == PR_POLY - 1) {
-              y = pr_exp2_poly(x);
-            } else {
-              y = up2(x);
-              y.x = pr_exp2(y.x);
-              y.y = pr_exp2(y.y);
-            }
+            float2 y = up2(fma2(pk2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), cc, zz));
+            y.x = pr_exp2(y.x);
+            y.y = pr_exp2(y.y);
             sum[i % 2] = add2(sum[i % 2], pk2(y.x, y.y));
             const __half2 two = __floats2half2_rn(y.x, y.y);
             pk[i] = *reinterpret_cast<const uint32_t *>(&two);
@@ -422,9 +415,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         tc_fence_after();
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a row that sees nothing: zeros
         // through shared memory (Q has been read), so that rows are written whole
-#pragma unroll
-        for (int c = 0; c < DP / 32; ++c) {
-          if (c * 32 >= D) break;
+#pragma unroll 1
+        for (int c = 0; c * 32 < D; ++c) {
           uint32_t o[32];
           if (it.last[w] >= 0) {
             tmem_ld32(to + c * 32, o);
@@ -448,6 +440,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         }
         __syncwarp();
         uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R) * a.ldo + (int64_t)it.head * A.group * D;
+#pragma unroll 1
         for (int p = lane; p < 32 * chunks; p += 32) {
           const int r0 = (int)((p * by_chunks) >> 16), c = p - r0 * chunks, rr = q * 32 + r0;
           if (rr >= used) break;
@@ -460,6 +453,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ keys and values
+    regs_dec<W::REG_LOAD>();
+    constexpr int GROUPS = 8 / W::LOAD;  // 16 tokens each, of a tile's 8
     constexpr int ITER = DP / 16;  // 16-byte chunks of fp16 a lane holds of 16 rows
     const int chunks = D / 8, n = 2 * steps;
     const uint32_t recip = 65536u / chunks + 1;  // p / chunks = (p * recip) >> 16 for p < 256
@@ -471,7 +466,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       int64_t at, sat;
       uint32_t rows;
     };
-    auto token = [&](int j, int gi) { return pr_tile(it, j) * PR_T + (int)(w2 * 2 + gi) * 16; };
+    auto token = [&](int j, int gi) { return pr_tile(it, j) * PR_T + (int)(w2 * GROUPS + gi) * 16; };
     // the page's number is fetched a tile ahead
     auto page_of = [&](int j, int gi) -> int32_t {
       const int tok = token(j, gi);
@@ -508,7 +503,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
     };
     auto dst_of = [&](int gi, int p) -> uint32_t {
       const int r = (int)((p * recip) >> 16), c = p - r * chunks;
-      return (uint32_t)((c / 8) * (PR_T * 128)) + swz128((w2 * 2 + gi) * 16 + r, c % 8);
+      return (uint32_t)((c / 8) * (PR_T * 128)) + swz128((w2 * GROUPS + gi) * 16 + r, c % 8);
     };
     bool ok = true;
     if (!E4M3) {
@@ -549,22 +544,22 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
       if (ok)
         for (int v = max(0, n - PR_LAG); v < n; ++v) arrive(v);
     } else {
-      // a ring of this warp's own: 16 rows of keys (twice) and of values (twice), each
+      // a ring of this warp's own: 16 rows of keys and 16 of values, each
       // refilled for the next tile as soon as it has been converted
-      uint8_t *raw = base + (2 + S::SLOTS) * S::TILE + w2 * 4 * S::RAW;
-      int32_t page[2] = {page_of(0, 0), page_of(0, 1)};
-      Place pl[2];       // of the tile whose copies are under way
-      uint32_t rows[4];  // visible ones of the four pieces in the ring
-      uint32_t fetched[4] = {0, 0, 0, 0};
-      auto fetch = [&](int q) {  // piece q: keys (0, 1) or values (2, 3), 16 tokens q % 2
-        const Place &p = pl[q % 2];
+      uint8_t *raw = base + (2 + S::SLOTS) * S::TILE + w2 * 2 * S::RAW;
+      int32_t page = page_of(0, 0);
+      Place pl;          // of the tile whose copies are under way
+      uint32_t rows[2];  // visible ones of the pieces in the ring
+      uint32_t fetched[2] = {0, 0};
+      auto fetch = [&](int q) {  // piece q: keys (0) or values (1)
+        const Place &p = pl;
         rows[q] = p.rows;
         ++fetched[q];
         if (lane == 0) {
           uint64_t *bar = &bars->raw[w2][q];
           if (p.rows) {
-            const uint8_t *kv = (q < 2 ? a.c.k : a.c.v) + p.at;
-            const float *sc = (q < 2 ? a.c.ks : a.c.vs) + p.sat;
+            const uint8_t *kv = (q == 0 ? a.c.k : a.c.v) + p.at;
+            const float *sc = (q == 0 ? a.c.ks : a.c.vs) + p.sat;
             mbar_arrive_expect_tx(bar, 16 * D + 64);
             bulk_load(raw + q * S::RAW, kv, 16 * D, bar);
             bulk_load(raw + q * S::RAW + 16 * DP, sc, 64, bar);
@@ -574,25 +569,22 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
         }
       };
       auto places = [&](int j) {
-#pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-          pl[gi] = place(j, gi, page[gi]);
-          page[gi] = page_of(j + 1, gi);
-        }
+        pl = place(j, 0, page);
+        page = page_of(j + 1, 0);
       };
       if (steps > 0) {
         places(0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) fetch(q);
+        for (int q = 0; q < 2; ++q) fetch(q);
       }
       int j = 0;
       for (; j < steps && ok; ++j) {
         if (j + 1 < steps) places(j + 1);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int u = 2 * j + q / 2;
+        for (int q = 0; q < 2; ++q) {
+          const int u = 2 * j + q;
           bool fine = true;
-          if (q % 2 == 0 && u >= S::SLOTS) fine = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
+          if (u >= S::SLOTS) fine = pr_wait(bars, &bars->empty[u % S::SLOTS], (u / S::SLOTS - 1) & 1);
           fine = fine && pr_wait(bars, &bars->raw[w2][q], j & 1);
           ok = __all_sync(FULL, fine);
           if (!ok) break;
@@ -607,11 +599,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
             uint2 x[ITER];
 #pragma unroll
             for (int i = 0; i < ITER; ++i) x[i] = *reinterpret_cast<const uint2 *>(from + (i * 32 + lane) * 8);
-            uint8_t *to = st + ((lane % C) / 8) * (PR_T * 128) + (q % 2) * 2048;
+            uint8_t *to = st + ((lane % C) / 8) * (PR_T * 128);
 #pragma unroll
             for (int i = 0; i < ITER; ++i) {
               const int r = i * (32 / C) + lane / C;
-              *reinterpret_cast<uint4 *>(to + (w2 * 32 * 128) + swz128(r, lane % 8)) =
+              *reinterpret_cast<uint4 *>(to + (w2 * 16 * 128) + swz128(r, lane % 8)) =
                   pr_convert(x[i], __shfl_sync(FULL, one, r));
             }
           } else {
@@ -622,23 +614,24 @@ __global__ void __launch_bounds__(PR_THREADS, 1) k_attn_prompt(const PrArgs A) {
               if (p < 16 * chunks) {
                 uint4 x = pr_convert(*reinterpret_cast<const uint2 *>(from + p * 8), s2);
                 if (!((rows[q] >> r) & 1)) x = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(st + dst_of(q % 2, p)) = x;
+                *reinterpret_cast<uint4 *>(st + dst_of(0, p)) = x;
               }
             }
           }
           __syncwarp();  // the piece has been read
           if (j + 1 < steps) fetch(q);
-          if (q % 2) arrive(u);
+          arrive(u);
         }
       }
       if (!ok && lane == 0)  // copies under way land before the block ends
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
           if (!mbar_wait(&bars->raw[w2][q], (fetched[q] - 1) & 1, DRAIN_NS)) bars->undrained = 1;
     }
     if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
   } else {
     // ------------------------------------------------ MMA issue
+    regs_dec<W::REG_MMA>();
     // warp w issues the products of tile w, all lanes in step
     if (warp < 2 && steps > 0) {
       const int w = warp, n = __shfl_sync(FULL, steps, 0);
@@ -752,7 +745,7 @@ static cudaError_t launch_prompt_t(const PrArgs &A, int64_t blocks, cudaStream_t
   static SmemOptIn opt_in;
   auto kern = k_attn_prompt<DP, E4M3>;
   if (cudaError_t e = opt_in(kern, PrShape<DP, E4M3>::SMEM)) return e;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PR_THREADS), PrShape<DP, E4M3>::SMEM, s, A);
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PrWarps<E4M3>::THREADS), PrShape<DP, E4M3>::SMEM, s, A);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
