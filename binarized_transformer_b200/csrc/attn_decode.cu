@@ -8,27 +8,31 @@
 // m = max(m_a, m_b), l = l_a 2^(m_a - m) + l_b 2^(m_b - m), the same for the sums.
 //
 // Work: an item is a sequence's key head with up to 16 of its query heads, its
-// units are the tiles of 64 tokens that hold a visible key. All units of the
-// call in a row are cut into equal pieces, one for each block, so that lengths
-// of any mix load the GPU evenly and one long sequence is spread over all of
-// it. A block that covers an item alone writes the output; pieces of an item go
-// to the workspace (at most two of a block: one item that began before it, one
-// that goes on after it) and k_attn_join adds them in the order of the blocks, so
-// the order of every sum is fixed by the lengths alone.
+// units are the tiles (64 tokens, E4M3 128) that hold a visible key. All units of
+// the call in a row are cut into equal pieces, one for each block, so that lengths
+// of any mix load the GPU evenly and one long sequence is spread over all of it. A
+// block that covers an item alone writes the output; pieces of an item go to the
+// workspace (at most two of a block: one item that began before it, one that goes
+// on after it) and k_attn_join adds them in the order of the blocks, so the order
+// of every sum is fixed by the lengths alone.
 //
-// Inside a block each of the 4 warps takes 16 tokens of a tile. page_size is a
-// multiple of 16, so these lie in one page and are one contiguous piece of it.
+// Inside a block each of the 4 warps takes 16 (32) tokens of a tile. page_size is a
+// multiple of 16, so 16 tokens lie in one page and are one contiguous piece of it.
 // A warp copies its tokens into a ring of its own (cp.async, rows that are
 // hidden or past the end are filled with zeros and never read) and needs no
 // barrier but its own; the block meets only at the end of an item.
 //
-// The products run on mma.sync m16n8k16: the query heads of an item are the 16
-// rows, which suits 1 .. 16 heads on one key head; the fifth-generation
-// instructions would need 64 or 128 rows, and here HBM is the bound: per SM 23
-// bytes a clock, i.e. one such instruction every 11 clocks of a pipe that takes one
-// every 2. P is rounded to fp16 for the second product, l sums it unrounded.
-// E4M3: K's scale is applied to the scores in fp32; V's, a power of two, to the
-// converted values, which stays exact.
+// The products run on mma.sync m16n8k16, transposed: 16 keys are the rows and 8
+// query heads the columns (two such blocks for 9 .. 16 heads), then 16 columns of V
+// the rows. So a key converted or loaded once meets all heads in one instruction and
+// the running sums of 8 heads take 32 registers. The fifth-generation instructions
+// would need 64 or 128 rows, and here HBM is the bound: 23 bytes a clock and SM.
+//
+// The reference m follows the maximum only when a score passes it by 2^8 (weights
+// up to 2^8 are kept): most tiles then need no maximum over the lanes. P is rounded
+// to fp16 for the second product, l sums it unrounded. E4M3: K's scale is applied
+// to the scores in fp32; V's, a power of two, to the converted values, which stays
+// exact.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -36,30 +40,36 @@
 
 namespace bwta {
 
-constexpr int DEC_TILE = 64;     // tokens of a unit
 constexpr int DEC_WARPS = 4, DEC_THREADS = DEC_WARPS * 32;
-constexpr int DEC_SUB = DEC_TILE / DEC_WARPS;  // tokens of one warp in a unit
-constexpr int DEC_ROWS = 16;     // query heads of an item
-constexpr int DEC_MIN_UNITS = 1; // units that a block takes at least
+constexpr int DEC_MAX_ROWS = 16;  // query heads of an item at most
+constexpr int DEC_MIN_UNITS = 1;  // units that a block takes at least
 constexpr int DEC_MAX_BLOCKS = 640;
+constexpr float DEC_SLACK = 8.0f;  // how far scores may pass the reference (log2)
 constexpr int JOIN_THREADS = 256, JOIN_HEADS = JOIN_THREADS / 32;
 
-template <int DP, bool E4M3>
+__host__ __device__ constexpr int dec_tile(bool e4m3) { return e4m3 ? 128 : 64; }
+
+template <int DP, bool E4M3, int NB>
 struct DecShape {
+  static constexpr int SUB = dec_tile(E4M3) / DEC_WARPS;  // tokens of one warp in a unit
+  static constexpr int TILE = dec_tile(E4M3);
   static constexpr int ROW = DP * (E4M3 ? 1 : 2);      // bytes of a token's row in the ring
-  static constexpr int STAGES = E4M3 ? 6 : 3;
-  static constexpr int HALF = DEC_SUB * ROW;           // keys (or values) of a stage
-  static constexpr int STAGE = 2 * HALF + (E4M3 ? 2 * DEC_SUB * 4 : 0);
+  static constexpr int STAGES = DP == 64 ? 6 : 3;
+  static constexpr int HALF = SUB * ROW;               // keys (or values) of a stage
+  static constexpr int STAGE = 2 * HALF + (E4M3 ? 2 * SUB * 4 : 0);
   static constexpr int RING = DEC_WARPS * STAGES * STAGE;
-  static constexpr int PART = (DP / 2 + 4) * 32;       // floats of one warp's running values
-  static constexpr int SMEM = RING + 2 * PART * 4;
-  static_assert(2 * PART * 4 >= (DEC_THREADS + 1 + DEC_WARPS) * 8, "the prefix sums share the place");
+  static constexpr int PART = (DP / 16 * NB * 4 + 4 * NB) * 32;  // floats of one warp's running values
+  static constexpr int PARTS = NB == 1 ? 3 : 1;        // kept so that two blocks fit an SM
+  static constexpr int SMEM = RING + PARTS * PART * 4;
+  static_assert(PARTS * PART * 4 >= (DEC_THREADS + 1 + DEC_WARPS) * 8, "the prefix sums share the place");
+  static_assert(2 * (SMEM + 1024) <= 233472, "two blocks on an SM");
 };
 
 struct DecArgs {
   AttnArgs a;
   float *ws;
-  int groups;  // items of a key head: ceil(heads per key head / 16)
+  int groups;  // items of a key head
+  int per_item;  // query heads of one: 8 or 16
   int rows;    // heads of an item at most (rows of a piece in the workspace)
   int blocks;  // of k_attn_decode
 };
@@ -70,17 +80,18 @@ struct DecSeq {
   int32_t units;
   bool bad;
 };
+template <int TILE>
 __device__ __forceinline__ DecSeq dec_seq(const AttnArgs &a, int64_t s) {
   DecSeq q;
   q.bad = false;
   q.slot = kv_slot(a.r, s);
   q.len = kv_length(a.r, q.slot, a.c.ps, q.bad);
-  const int32_t tiles = (q.len + DEC_TILE - 1) / DEC_TILE;
+  const int32_t tiles = (q.len + TILE - 1) / TILE;
   q.sink_tiles = 0;
   q.first = 0;
   if (a.window && a.window < q.len) {
-    q.first = (int32_t)((q.len - a.window) / DEC_TILE);
-    q.sink_tiles = min((int32_t)((min(a.sinks, (int64_t)q.len) + DEC_TILE - 1) / DEC_TILE), q.first);
+    q.first = (int32_t)((q.len - a.window) / TILE);
+    q.sink_tiles = min((int32_t)((min(a.sinks, (int64_t)q.len) + TILE - 1) / TILE), q.first);
   }
   q.units = q.sink_tiles + tiles - q.first;
   return q;
@@ -88,13 +99,13 @@ __device__ __forceinline__ DecSeq dec_seq(const AttnArgs &a, int64_t s) {
 
 // Units before each thread's share of the sequences (a share is `per` sequences),
 // for blocks of T threads; before[T] = all of them.
-template <int T>
+template <int T, int TILE>
 __device__ __forceinline__ int dec_scan(const AttnArgs &a, int64_t *before, int64_t *sums) {
   const int per = (int)ceil_div<int64_t>(a.n_seq, T);
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int64_t s = (int64_t)threadIdx.x * per + i;
-    if (s < a.n_seq) mine += dec_seq(a, s).units;
+    if (s < a.n_seq) mine += dec_seq<TILE>(a, s).units;
   }
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int64_t x = mine;
@@ -190,20 +201,29 @@ __device__ __forceinline__ uint32_t ring_at(int r, int c) {
   return (uint32_t)(r * ROW + ((c ^ (ROW == 64 ? (r >> 1) & 3 : r & 7)) << 4));
 }
 
+// 8x8 halves, transposed among the lanes of a warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // A position in a block's units: sequence, item, tile.
+template <int TILE>
 struct DecCursor {
   int64_t s;
   DecSeq q;
   int item, unit;  // item of the sequence, unit of the item
   __device__ void enter(const AttnArgs &a) {  // the first sequence with units from s on
-    while (q.units == 0) q = dec_seq(a, ++s);
+    while (q.units == 0) q = dec_seq<TILE>(a, ++s);
   }
   __device__ int tile() const { return unit < q.sink_tiles ? unit : q.first + unit - q.sink_tiles; }
 };
 
-template <int DP, bool E4M3>
+template <int DP, bool E4M3, int NB>
 __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A) {
-  using S = DecShape<DP, E4M3>;
+  using S = DecShape<DP, E4M3, NB>;
+  constexpr int SUB = S::SUB, TILE = S::TILE, MT = SUB / 16, KS = DP / 16, ROWS = 8 * NB;
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnArgs &a = A.a;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
@@ -217,7 +237,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
     for (int i = threadIdx.x * 16; i < S::RING; i += DEC_THREADS * 16)
       *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0, 0, 0, 0);
   pdl_wait();
-  const int per = dec_scan<DEC_THREADS>(a, before, sums);  // its barriers cover the zeros
+  const int per = dec_scan<DEC_THREADS, TILE>(a, before, sums);  // its barriers cover the zeros
   const DecCut cut(before[DEC_THREADS] * items, A.blocks);
   if ((int)blockIdx.x >= cut.blocks) return;
   const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
@@ -225,7 +245,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
   if (n == 0) return;
 
   // the sequence, item and tile of unit u0
-  DecCursor at;
+  DecCursor<TILE> at;
   {
     int lo = 0, hi = DEC_THREADS - 1;
     while (lo < hi) {
@@ -235,104 +255,132 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
     }
     int64_t u = u0 - before[lo] * items;
     at.s = (int64_t)lo * per;
-    at.q = dec_seq(a, at.s);
+    at.q = dec_seq<TILE>(a, at.s);
     while (u >= (int64_t)at.q.units * items) {
       u -= (int64_t)at.q.units * items;
-      at.q = dec_seq(a, ++at.s);
+      at.q = dec_seq<TILE>(a, ++at.s);
     }
     at.item = (int)(u / at.q.units);
     at.unit = (int)(u - (int64_t)at.item * at.q.units);
   }
   __syncthreads();  // the prefix sums have been read: `joint` may be written
-  DecCursor ld = at;  // runs ahead of `at`: the copies
-  int loaded = 0;
   bool bad = false, finite = true;
 
-  // page of ld's tokens, fetched one unit before it is used
-  auto page_of = [&](const DecCursor &c) -> int32_t {
-    const int64_t tok = (int64_t)c.tile() * DEC_TILE + warp * DEC_SUB;
-    return tok < c.q.len ? a.r.pages[(int64_t)c.q.slot * a.r.ld + tok / a.c.ps] : -1;
+  // ---- the copies run ahead: their own position, with the entry of the row of pages
+  // (idx) and the token in that page (in) that this warp's first token falls on
+  DecCursor<TILE> ld = at;
+  int loaded = 0, idx = 0, in = 0;
+  const int step_idx = TILE / a.c.ps, step_in = TILE - step_idx * a.c.ps;
+  int32_t page[MT];  // fetched one unit before they are used
+  auto first_token = [&](const DecCursor<TILE> &c) { return c.tile() * TILE + warp * SUB; };
+  auto locate = [&]() {
+    const int tok = first_token(ld);
+    idx = tok / a.c.ps;
+    in = tok - idx * a.c.ps;
   };
-  auto step = [&](DecCursor &c) {
-    if (++c.unit < c.q.units) return;
+  auto fetch_pages = [&]() {
+    const int tok = first_token(ld);
+    const int32_t *row = a.r.pages + (int64_t)ld.q.slot * a.r.ld + idx;
+#pragma unroll
+    for (int h = 0; h < MT; ++h)
+      page[h] = tok + 16 * h < ld.q.len ? row[h && in + 16 >= a.c.ps ? 1 : 0] : -1;
+  };
+  auto step = [&](DecCursor<TILE> &c) -> bool {  // true: not simply the next tile
+    if (++c.unit < c.q.units) return c.unit == c.q.sink_tiles;
     c.unit = 0;
-    if (++c.item < items) return;
+    if (++c.item < items) return true;
     c.item = 0;
-    c.q = dec_seq(a, ++c.s);
+    c.q = dec_seq<TILE>(a, ++c.s);
     c.enter(a);
+    return true;
   };
-  int32_t page = page_of(ld);
+  // which chunks of a 512-byte stretch this lane copies, and where they land
+  constexpr int CH = S::ROW / 16, RPI = 32 / CH;  // chunks of a row, rows a copy of the warp covers
   auto load = [&]() {
     if (loaded < n) {
-      const int tok = ld.tile() * DEC_TILE + warp * DEC_SUB, kh = ld.item / A.groups;
-      const int rows = min(DEC_SUB, ld.q.len - tok);
-      if (rows > 0) {
-        const bool ok = (uint32_t)page < (uint32_t)a.c.num_pages;
+      const int tok = first_token(ld), kh = ld.item / A.groups;
+      const uint32_t st = ring + (loaded % S::STAGES) * S::STAGE;
+      const bool plain = tok + SUB <= ld.q.len &&
+                         (!a.window || tok >= ld.q.len - a.window || tok + SUB <= a.sinks);
+#pragma unroll
+      for (int h = 0; h < MT; ++h) {
+        const int tk = tok + 16 * h, rows = min(16, ld.q.len - tk);
+        if (rows <= 0) break;
+        const int inp = h && in + 16 >= a.c.ps ? 0 : in + 16 * h;
+        const bool ok = (uint32_t)page[h] < (uint32_t)a.c.num_pages;
         bad |= !ok;
-        const int64_t row = (int64_t)kh * a.c.ps + tok % a.c.ps;
-        const int64_t elt = (int64_t)(ok ? page : 0) * a.c.page_stride + row * D;
+        const int64_t row = (int64_t)kh * a.c.ps + inp;
+        const int64_t elt = (int64_t)(ok ? page[h] : 0) * a.c.page_stride + row * D;
         const uint8_t *k = a.c.k + (E4M3 ? elt : 2 * elt), *v = a.c.v + (E4M3 ? elt : 2 * elt);
-        const uint32_t st = ring + (loaded % S::STAGES) * S::STAGE;
-        // visible rows of the 16: below `rows`, and not between the sinks and the window
-        const int gap0 = a.window ? (int)min(max(a.sinks - tok, (int64_t)0), (int64_t)DEC_SUB) : DEC_SUB;
-        const int gap1 = a.window ? (int)min(max(ld.q.len - a.window - tok, (int64_t)0), (int64_t)DEC_SUB) : 0;
-        auto seen = [&](int r) { return ok && r < rows && (r < gap0 || r >= gap1); };
-        const int width = D * (E4M3 ? 1 : 2);
-        if (!E4M3 || D % 16 == 0) {
-          const int chunks = width / 16;
-          if (chunks == S::ROW / 16) {
+        const uint32_t to = st + h * 16 * S::ROW;
+        if (plain && ok && D == DP) {
 #pragma unroll
-            for (int i = 0; i < S::HALF / 512; ++i) {
-              const int p = i * 32 + lane, r = p / (S::ROW / 16), c = p % (S::ROW / 16);
-              cp_async16(st + ring_at<S::ROW>(r, c), k + p * 16, seen(r));
-            }
+          for (int i = 0; i < 16 / RPI; ++i)
+            cp_async16(to + ring_at<S::ROW>(i * RPI + lane / CH, lane % CH), k + (i * 32 + lane) * 16, true);
 #pragma unroll
-            for (int i = 0; i < S::HALF / 512; ++i) {
-              const int p = i * 32 + lane, r = p / (S::ROW / 16), c = p % (S::ROW / 16);
-              cp_async16(st + S::HALF + ring_at<S::ROW>(r, c), v + p * 16, seen(r));
-            }
-          } else {
-            for (int p = lane; p < DEC_SUB * chunks; p += 32) {
+          for (int i = 0; i < 16 / RPI; ++i)
+            cp_async16(to + S::HALF + ring_at<S::ROW>(i * RPI + lane / CH, lane % CH), v + (i * 32 + lane) * 16, true);
+        } else {
+          // visible rows of the 16: below `rows`, and not between the sinks and the window
+          const int gap0 = a.window ? (int)min(max(a.sinks - tk, (int64_t)0), (int64_t)16) : 16;
+          const int gap1 = a.window ? (int)min(max(ld.q.len - a.window - tk, (int64_t)0), (int64_t)16) : 0;
+          auto seen = [&](int r) { return ok && r < rows && (r < gap0 || r >= gap1); };
+          const int width = D * (E4M3 ? 1 : 2);
+          if (!E4M3 || D % 16 == 0) {
+            const int chunks = width / 16;
+            for (int p = lane; p < 16 * chunks; p += 32) {
               const int r = p / chunks, c = p - r * chunks;
-              const uint32_t to = st + ring_at<S::ROW>(r, c);
-              cp_async16(to, k + p * 16, seen(r));
-              cp_async16(to + S::HALF, v + p * 16, seen(r));
+              const uint32_t at16 = to + ring_at<S::ROW>(r, c);
+              cp_async16(at16, k + p * 16, seen(r));
+              cp_async16(at16 + S::HALF, v + p * 16, seen(r));
             }
-          }
-        } else {  // rows of 8 bytes more than a multiple of 16
-          const int pieces = width / 8;
-          for (int p = lane; p < DEC_SUB * pieces; p += 32) {
-            const int r = p / pieces, c = p - r * pieces;
-            const uint32_t to = st + ring_at<S::ROW>(r, c / 2) + (c & 1) * 8;
-            cp_async8(to, k + p * 8, seen(r));
-            cp_async8(to + S::HALF, v + p * 8, seen(r));
+          } else {  // rows of 8 bytes more than a multiple of 16
+            const int pieces = width / 8;
+            for (int p = lane; p < 16 * pieces; p += 32) {
+              const int r = p / pieces, c = p - r * pieces;
+              const uint32_t at8 = to + ring_at<S::ROW>(r, c / 2) + (c & 1) * 8;
+              cp_async8(at8, k + p * 8, seen(r));
+              cp_async8(at8 + S::HALF, v + p * 8, seen(r));
+            }
           }
         }
-        if (E4M3 && lane < 8) {  // the rows' scales: 4 x 16 bytes of k, then of v
+        if (E4M3 && lane < 8) {  // the rows' scales: SUB of k, then of v
           const int c = lane % 4;
-          const float *src = (lane < 4 ? a.c.ks : a.c.vs) + (int64_t)(ok ? page : 0) * a.c.scale_stride + row;
-          cp_async16(st + 2 * S::HALF + lane * 16, src + c * 4, ok && c * 4 < rows);
+          const float *src = (lane < 4 ? a.c.ks : a.c.vs) + (int64_t)(ok ? page[h] : 0) * a.c.scale_stride + row;
+          cp_async16(st + 2 * S::HALF + ((lane / 4) * SUB + h * 16 + c * 4) * 4, src + c * 4, ok && c * 4 < rows);
         }
       }
       if (++loaded < n) {
-        step(ld);
-        page = page_of(ld);
+        if (step(ld)) {
+          locate();
+        } else {
+          idx += step_idx;
+          in += step_in;
+          if (in >= a.c.ps) {
+            in -= a.c.ps;
+            ++idx;
+          }
+        }
+        fetch_pages();
       }
     }
     cp_commit();
   };
-
+  locate();
+  fetch_pages();
 #pragma unroll
   for (int i = 0; i < S::STAGES - 1; ++i) load();
 
-  constexpr int KS = DP / 16;
-  uint32_t qa[KS][4];
-  float o[DP / 8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+  // ---- the running values: columns of the tiles are heads 8 b + 2 t, + 1
+  uint32_t qb[NB][KS][2];
+  float o[NB][KS][4], m[NB][2], l[NB][2];
   const float c2 = a.scale * 1.44269504088896340736f;
+  const int mat = lane / 8, mr = lane % 8;
   bool fresh = true;
+  int stage = 0;
   for (int i = 0; i < n; ++i) {
-    const int kh = at.item / A.groups, h0 = (at.item % A.groups) * DEC_ROWS;
-    const int mine = min(DEC_ROWS, heads - h0);  // heads of this item
+    const int kh = at.item / A.groups, h0 = (at.item - kh * A.groups) * ROWS;
+    const int mine = min(ROWS, heads - h0);  // heads of this item
     if (fresh) {
       fresh = false;
       const uint16_t *q = a.q + at.s * a.ldq + (int64_t)(kh * heads + h0) * D;
@@ -342,209 +390,266 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
         return r < mine && d < D ? *reinterpret_cast<const uint32_t *>(q + (int64_t)r * D + d) : 0u;
       };
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int d0 = ks * 16 + (E4M3 ? 4 * t : 2 * t), d1 = d0 + (E4M3 ? 2 : 8);
-        qa[ks][0] = two(g, d0);
-        qa[ks][1] = two(g + 8, d0);
-        qa[ks][2] = two(g, d1);
-        qa[ks][3] = two(g + 8, d1);
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int d0 = ks * 16 + (E4M3 ? 4 * t : 2 * t), d1 = d0 + (E4M3 ? 2 : 8);
+          qb[b][ks][0] = two(8 * b + g, d0);
+          qb[b][ks][1] = two(8 * b + g, d1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[b][ks][e] = 0.0f;
+        }
+        m[b][0] = m[b][1] = -INFINITY;
+        l[b][0] = l[b][1] = 0.0f;
       }
-#pragma unroll
-      for (int j = 0; j < DP / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.0f;
     }
     load();
     cp_wait<S::STAGES - 1>();
     __syncwarp();
-    const int tok = at.tile() * DEC_TILE + warp * DEC_SUB;
+    const int tok = first_token(at);
     bad |= at.q.bad;
     if (tok < at.q.len) {
-      const uint32_t st = ring + (i % S::STAGES) * S::STAGE;
-      float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0};
+      const uint32_t st = ring + stage * S::STAGE;
+      float s[MT][NB][4];
+#pragma unroll
+      for (int h = 0; h < MT; ++h)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[h][b][e] = 0.0f;
       uint32_t r[4];
-      const int mat = lane / 8, mr = lane % 8;
-      if (!E4M3) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          ldsm4(st + ring_at<S::ROW>((mat / 2) * 8 + mr, ks * 2 + (mat & 1)), r);
-          mma16816(s0, qa[ks], r[0], r[1]);
-          mma16816(s1, qa[ks], r[2], r[3]);
-        }
-      } else {
+      for (int h = 0; h < MT; ++h) {
+        if (!E4M3) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ks += 2) {
-          ldsm4(st + ring_at<S::ROW>((mat & 1) * 8 + mr, ks + mat / 2), r);
-          mma16816(s0, qa[ks], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
-          mma16816(s1, qa[ks], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
-          mma16816(s0, qa[ks + 1], e4m3x2_to_half2(r[2]), e4m3x2_to_half2(r[2] >> 16));
-          mma16816(s1, qa[ks + 1], e4m3x2_to_half2(r[3]), e4m3x2_to_half2(r[3] >> 16));
-        }
-      }
-      // scores: columns 2t, 2t+1 of s0 are tokens tok + 2t .., of s1 tok + 8 + 2t ..
-      float f[4] = {c2, c2, c2, c2};
-      const int64_t lo = a.window ? at.q.len - a.window : 0;
-      bool vis[4];
+          for (int ks = 0; ks < KS; ++ks) {
+            ldsm4(st + ring_at<S::ROW>(h * 16 + (mat & 1) * 8 + mr, ks * 2 + mat / 2), r);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = tok + (e / 2) * 8 + 2 * t + (e & 1);
-        vis[e] = j < at.q.len && (j >= lo || j < a.sinks);
-      }
-      uint32_t vs01 = 0, vs23 = 0;
-      if (E4M3) {
-        const float2 *sc = reinterpret_cast<const float2 *>(smem + (st - smem_addr(smem)) + 2 * S::HALF);
-        const float2 ka = sc[t], kb = sc[t + 4], va = sc[8 + t], vb = sc[12 + t];
-        f[0] *= ka.x;
-        f[1] *= ka.y;
-        f[2] *= kb.x;
-        f[3] *= kb.y;
-        // a hidden token's scale may be anything, and its weight of 0 would not undo a NaN
-        vs01 = half2_bits(vis[0] ? va.x : 0.0f, vis[1] ? va.y : 0.0f);
-        vs23 = half2_bits(vis[2] ? vb.x : 0.0f, vis[3] ? vb.y : 0.0f);
-      }
-      float x[2][4];
+            for (int b = 0; b < NB; ++b) mma16816(s[h][b], r, qb[b][ks][0], qb[b][ks][1]);
+          }
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[0][e] = vis[e] ? (e < 2 ? s0[e] : s1[e - 2]) * f[e] : -INFINITY;
-        x[1][e] = vis[e] ? (e < 2 ? s0[e + 2] : s1[e]) * f[e] : -INFINITY;
-      }
-      float n0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
-      float n1 = fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]));
+          for (int ks = 0; ks < KS; ks += 2) {
+            ldsm4(st + ring_at<S::ROW>(h * 16 + (mat & 1) * 8 + mr, ks + mat / 2), r);
 #pragma unroll
-      for (int d = 1; d < 4; d *= 2) {
-        n0 = fmaxf(n0, __shfl_xor_sync(FULL, n0, d));
-        n1 = fmaxf(n1, __shfl_xor_sync(FULL, n1, d));
-      }
-      n0 = fmaxf(n0, m0);
-      n1 = fmaxf(n1, m1);
-      if (__any_sync(FULL, n0 > m0 || n1 > m1)) {
-        // nothing seen so far: the sums are zero and the factor does not matter
-        const float a0 = m0 == -INFINITY ? 0.0f : exp2_fast(m0 - n0);
-        const float a1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= a0;
-        l1 *= a1;
+            for (int p = 0; p < 2; ++p) {
+              const uint32_t ka[4] = {e4m3x2_to_half2(r[2 * p]), e4m3x2_to_half2(r[2 * p + 1]),
+                                      e4m3x2_to_half2(r[2 * p] >> 16), e4m3x2_to_half2(r[2 * p + 1] >> 16)};
 #pragma unroll
-        for (int j = 0; j < DP / 8; ++j) {
-          o[j][0] *= a0;
-          o[j][1] *= a0;
-          o[j][2] *= a1;
-          o[j][3] *= a1;
+              for (int b = 0; b < NB; ++b) mma16816(s[h][b], ka, qb[b][ks + p][0], qb[b][ks + p][1]);
+            }
+          }
         }
       }
-      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-      float w[2][4];
+      // scores: rows g and g + 8 of each 16 tokens, columns 2t, 2t + 1
+      const float *scales = reinterpret_cast<const float *>(smem + (st - smem_addr(smem)) + 2 * S::HALF);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[0][e] = exp2_fast(x[0][e] - z0);
-        w[1][e] = exp2_fast(x[1][e] - z1);
-      }
-      l0 += (w[0][0] + w[0][1]) + (w[0][2] + w[0][3]);
-      l1 += (w[1][0] + w[1][1]) + (w[1][2] + w[1][3]);
-      const uint32_t pa[4] = {half2_bits(w[0][0], w[0][1]), half2_bits(w[1][0], w[1][1]),
-                              half2_bits(w[0][2], w[0][3]), half2_bits(w[1][2], w[1][3])};
-      if (!E4M3) {
+      for (int h = 0; h < MT; ++h)
 #pragma unroll
-        for (int j = 0; j < DP / 16; ++j) {
-          ldsm4t(st + S::HALF + ring_at<S::ROW>((mat & 1) * 8 + mr, j * 2 + mat / 2), r);
-          mma16816(o[2 * j], pa, r[0], r[1]);
-          mma16816(o[2 * j + 1], pa, r[2], r[3]);
+        for (int e = 0; e < 2; ++e) {
+          const float f = E4M3 ? c2 * scales[h * 16 + e * 8 + g] : c2;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            s[h][b][2 * e] *= f;
+            s[h][b][2 * e + 1] *= f;
+          }
         }
-      } else {
-        // o[2j] holds the even columns of the j-th 16, o[2j + 1] the odd ones
+      const bool plain = tok + SUB <= at.q.len &&
+                         (!a.window || tok >= at.q.len - a.window || tok + SUB <= a.sinks);
+      if (!plain) {
+        const int64_t lo = a.window ? at.q.len - a.window : 0;
 #pragma unroll
-        for (int j = 0; j < DP / 16; j += 2) {
-          ldsm4t(st + S::HALF + ring_at<S::ROW>((mat & 1) * 8 + mr, j + mat / 2), r);
+        for (int h = 0; h < MT; ++h)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint32_t a0 = r[2 * p], b0 = r[2 * p + 1];
-            mma16816(o[2 * (j + p)], pa, mul_half2(e4m3x2_to_half2(__byte_perm(a0, 0, 0x20)), vs01),
-                     mul_half2(e4m3x2_to_half2(__byte_perm(b0, 0, 0x20)), vs23));
-            mma16816(o[2 * (j + p) + 1], pa, mul_half2(e4m3x2_to_half2(__byte_perm(a0, 0, 0x31)), vs01),
-                     mul_half2(e4m3x2_to_half2(__byte_perm(b0, 0, 0x31)), vs23));
+          for (int e = 0; e < 2; ++e) {
+            const int j = tok + h * 16 + e * 8 + g;
+            if (!(j < at.q.len && (j >= lo || j < a.sinks)))
+#pragma unroll
+              for (int b = 0; b < NB; ++b) s[h][b][2 * e] = s[h][b][2 * e + 1] = -INFINITY;
+          }
+      }
+      bool up = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[0][b][e], s[0][b][2 + e]);
+          if (MT == 2) x = fmaxf(fmaxf(x, s[MT - 1][b][e]), s[MT - 1][b][2 + e]);
+          up |= x > m[b][e] + DEC_SLACK;  // also from -infinity
+        }
+      if (__any_sync(FULL, up)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[0][b][e], s[0][b][2 + e]);
+            if (MT == 2) x = fmaxf(fmaxf(x, s[MT - 1][b][e]), s[MT - 1][b][2 + e]);
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(FULL, x, d));
+            const float mn = fmaxf(m[b][e], x);
+            // nothing seen so far: the sums are zero and the factor does not matter
+            const float f = m[b][e] == -INFINITY ? 0.0f : exp2_fast(m[b][e] - mn);
+            m[b][e] = mn;
+            l[b][e] *= f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              o[b][ks][e] *= f;
+              o[b][ks][2 + e] *= f;
+            }
+          }
+      }
+      uint32_t pb[MT][NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float z0 = m[b][0] == -INFINITY ? 0.0f : m[b][0], z1 = m[b][1] == -INFINITY ? 0.0f : m[b][1];
+#pragma unroll
+        for (int h = 0; h < MT; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w0 = exp2_fast(s[h][b][2 * e] - z0), w1 = exp2_fast(s[h][b][2 * e + 1] - z1);
+            l[b][0] += w0;
+            l[b][1] += w1;
+            pb[h][b][e] = transpose8(half2_bits(w0, w1));
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < MT; ++h) {
+        if (h > 0 && tok + 16 * h >= at.q.len) break;  // nothing was copied there
+        if (!E4M3) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            ldsm4t(st + S::HALF + ring_at<S::ROW>(h * 16 + (mat / 2) * 8 + mr, ks * 2 + (mat & 1)), r);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816(o[b][ks], r, pb[h][b][0], pb[h][b][1]);
+          }
+        } else {
+          // rows g of a product are the even columns of 16, rows g + 8 the odd ones
+          const float2 va = *reinterpret_cast<const float2 *>(scales + SUB + h * 16 + 2 * t);
+          const float2 vb = *reinterpret_cast<const float2 *>(scales + SUB + h * 16 + 8 + 2 * t);
+          uint32_t v01 = half2_bits(va.x, va.y), v23 = half2_bits(vb.x, vb.y);
+          if (!plain) {
+            // a hidden token's scale may be anything, and its weight of 0 would not undo a NaN
+            const int64_t lo = a.window ? at.q.len - a.window : 0;
+            auto vis = [&](int x) {
+              const int j = tok + h * 16 + x;
+              return j < at.q.len && (j >= lo || j < a.sinks);
+            };
+            v01 = half2_bits(vis(2 * t) ? va.x : 0.0f, vis(2 * t + 1) ? va.y : 0.0f);
+            v23 = half2_bits(vis(8 + 2 * t) ? vb.x : 0.0f, vis(9 + 2 * t) ? vb.y : 0.0f);
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ks += 2) {
+            ldsm4t(st + S::HALF + ring_at<S::ROW>(h * 16 + (mat & 1) * 8 + mr, ks + mat / 2), r);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const uint32_t x = r[2 * p], y = r[2 * p + 1];
+              const uint32_t vv[4] = {mul_half2(e4m3x2_to_half2(__byte_perm(x, 0, 0x20)), v01),
+                                      mul_half2(e4m3x2_to_half2(__byte_perm(x, 0, 0x31)), v01),
+                                      mul_half2(e4m3x2_to_half2(__byte_perm(y, 0, 0x20)), v23),
+                                      mul_half2(e4m3x2_to_half2(__byte_perm(y, 0, 0x31)), v23)};
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816(o[b][ks + p], vv, pb[h][b][0], pb[h][b][1]);
+            }
           }
         }
       }
     }
     __syncwarp();  // the stage may be filled again
+    if (++stage == S::STAGES) stage = 0;
 
     const bool item_ends = at.unit + 1 == at.q.units;
     if (item_ends || i == n - 1) {
-      // join the warps: 1 into 0 and 3 into 2, then 2 into 0
-      const int most = mine > 8 ? 4 : 2;  // rows g + 8 hold heads
+      // join the warps: 1, 2 and 3 into 0
 #pragma unroll
-      for (int d = 1; d < 4; d *= 2) {
-        l0 += __shfl_xor_sync(FULL, l0, d);
-        l1 += __shfl_xor_sync(FULL, l1, d);
-      }
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[b][e] += __shfl_xor_sync(FULL, l[b][e], d);
       auto give = [&](float *p) {
-        p[lane] = m0;
-        p[32 + lane] = l0;
-        p[64 + lane] = m1;
-        p[96 + lane] = l1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < most)
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
-            for (int j = 0; j < DP / 8; ++j) p[(4 + e * (DP / 8) + j) * 32 + lane] = o[j][e];
-      };
-      auto join = [&](float &m, float &l, float pm, float pl, float &fa, float &fb) {
-        const float M = fmaxf(m, pm);
-        fa = m == -INFINITY ? 0.0f : exp2_fast(m - M);
-        fb = pm == -INFINITY ? 0.0f : exp2_fast(pm - M);
-        l = l * fa + pl * fb;
-        m = M;
+          for (int e = 0; e < 2; ++e) {
+            p[(b * 4 + 2 * e) * 32 + lane] = m[b][e];
+            p[(b * 4 + 2 * e + 1) * 32 + lane] = l[b][e];
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[(4 * NB + (b * KS + ks) * 4 + e) * 32 + lane] = o[b][ks][e];
+        }
       };
       auto take = [&](const float *p) {
-        float fa[2], fb[2];
-        join(m0, l0, p[lane], p[32 + lane], fa[0], fb[0]);
-        join(m1, l1, p[64 + lane], p[96 + lane], fa[1], fb[1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < most)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < DP / 8; ++j)
-              o[j][e] = o[j][e] * fa[e / 2] + p[(4 + e * (DP / 8) + j) * 32 + lane] * fb[e / 2];
+          for (int e = 0; e < 2; ++e) {
+            const float pm = p[(b * 4 + 2 * e) * 32 + lane], pl = p[(b * 4 + 2 * e + 1) * 32 + lane];
+            const float M = fmaxf(m[b][e], pm);
+            const float fa = m[b][e] == -INFINITY ? 0.0f : exp2_fast(m[b][e] - M);
+            const float fb = pm == -INFINITY ? 0.0f : exp2_fast(pm - M);
+            l[b][e] = l[b][e] * fa + pl * fb;
+            m[b][e] = M;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int x = e; x < 4; x += 2)
+                o[b][ks][x] = o[b][ks][x] * fa + p[(4 * NB + (b * KS + ks) * 4 + x) * 32 + lane] * fb;
+          }
       };
-      if (warp & 1) give(joint + (warp / 2) * S::PART);
-      __syncthreads();
-      if (!(warp & 1)) take(joint + (warp / 2) * S::PART);
-      if (warp == 2) give(joint + S::PART);
-      __syncthreads();
-      if (warp == 0) take(joint + S::PART);
-      __syncthreads();
+      if (S::PARTS == 3) {
+        if (warp > 0) give(joint + (warp - 1) * S::PART);
+        __syncthreads();
+        if (warp == 0)
+#pragma unroll 1
+          for (int x = 0; x < 3; ++x) take(joint + x * S::PART);
+        __syncthreads();
+      } else {
+#pragma unroll 1
+        for (int x = 1; x < DEC_WARPS; ++x) {
+          if (warp == x) give(joint);
+          __syncthreads();
+          if (warp == 0) take(joint);
+          __syncthreads();
+        }
+      }
       if (warp == 0) {
         const bool began = i >= at.unit;  // the item's first unit is this block's too
         const bool whole = began && item_ends;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int row = g + 8 * half;
-          if (row >= mine) continue;
-          const float M = half ? m1 : m0, L = half ? l1 : l0;
-          float *piece = A.ws + (((size_t)blockIdx.x * 2 + (began ? 1 : 0)) * A.rows + row) * (DP + 2);
-          uint16_t *out = a.out + at.s * a.ldo + (int64_t)(kh * heads + h0 + row) * D;
-          if (!whole && t == 0) *reinterpret_cast<float2 *>(piece + DP) = make_float2(M, L);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j) {
-            // E4M3: even columns in o[2i], odd ones in o[2i + 1]; two neighbours at once
-            const int jj = E4M3 ? j & ~1 : j, e = E4M3 ? j & 1 : 0;
-            const int col = E4M3 ? (j / 2) * 16 + 4 * t + 2 * e : j * 8 + 2 * t;
-            float y0 = E4M3 ? o[jj][2 * half + e] : o[j][2 * half];
-            float y1 = E4M3 ? o[jj + 1 < DP / 8 ? jj + 1 : jj][2 * half + e] : o[j][2 * half + 1];
-            if (col >= D) continue;
-            if (whole) {
-              y0 /= L;
-              y1 /= L;
-              finite &= y0 - y0 == 0.0f && y1 - y1 == 0.0f;
-              *reinterpret_cast<uint32_t *>(out + col) = half2_bits(y0, y1);
-            } else {
-              *reinterpret_cast<float2 *>(piece + col) = make_float2(y0, y1);
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * b + 2 * t + e;
+            if (row >= mine) continue;
+            float *piece = A.ws + (((size_t)blockIdx.x * 2 + (began ? 1 : 0)) * A.rows + row) * (DP + 2);
+            uint16_t *out = a.out + at.s * a.ldo + (int64_t)(kh * heads + h0 + row) * D;
+            if (!whole && g == 0) *reinterpret_cast<float2 *>(piece + DP) = make_float2(m[b][e], l[b][e]);
+            const float inv = 1.0f / l[b][e];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const float y0 = o[b][ks][e], y1 = o[b][ks][2 + e];
+              const int c0 = ks * 16 + (E4M3 ? 2 * g : g), c1 = c0 + (E4M3 ? 1 : 8);
+              if (E4M3) {  // two neighbours
+                if (c0 >= D) continue;
+                if (whole) *reinterpret_cast<uint32_t *>(out + c0) = half2_bits(y0 * inv, y1 * inv);
+                else *reinterpret_cast<float2 *>(piece + c0) = make_float2(y0, y1);
+                if (whole) finite &= y0 * inv - y0 * inv == 0.0f && y1 * inv - y1 * inv == 0.0f;
+              } else {
+                if (c0 < D) {
+                  if (whole) out[c0] = __half_as_ushort(__float2half_rn(y0 * inv));
+                  else piece[c0] = y0;
+                  if (whole) finite &= y0 * inv - y0 * inv == 0.0f;
+                }
+                if (c1 < D) {
+                  if (whole) out[c1] = __half_as_ushort(__float2half_rn(y1 * inv));
+                  else piece[c1] = y1;
+                  if (whole) finite &= y1 * inv - y1 * inv == 0.0f;
+                }
+              }
             }
           }
-        }
       }
       fresh = true;
     }
@@ -557,7 +662,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
 
 // The outputs of items that several blocks share, and of empty sequences. A warp
 // a query head, 4 columns a lane.
-template <int DP>
+template <int DP, int TILE>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
   __shared__ int64_t before[JOIN_THREADS + 1], sums[JOIN_THREADS / 32];
   const AttnArgs &a = A.a;
@@ -568,9 +673,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
   const int D = a.c.D, heads = a.n_heads / a.c.H, items = a.c.H * A.groups;
   pdl_trigger();
   pdl_wait();
-  const int per = dec_scan<JOIN_THREADS>(a, before, sums);
+  const int per = dec_scan<JOIN_THREADS, TILE>(a, before, sums);
   if (h >= a.n_heads) return;
-  const DecSeq q = dec_seq(a, s);
+  const DecSeq q = dec_seq<TILE>(a, s);
   uint16_t *out = a.out + s * a.ldo + (int64_t)h * D + lane * 4;
   if (q.units == 0) {
     if (q.bad && lane == 0 && h == 0) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
@@ -578,13 +683,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
     return;
   }
   const DecCut cut(before[JOIN_THREADS] * items, A.blocks);
-  const int who = (int)(s / per), kh = h / heads, hg = (h - kh * heads) / DEC_ROWS;
+  const int who = (int)(s / per), kh = h / heads, hg = (h - kh * heads) / A.per_item;
   int64_t u = before[who] * items;
-  for (int64_t i = (int64_t)who * per; i < s; ++i) u += (int64_t)dec_seq(a, i).units * items;
+  for (int64_t i = (int64_t)who * per; i < s; ++i) u += (int64_t)dec_seq<TILE>(a, i).units * items;
   u += (int64_t)(kh * A.groups + hg) * q.units;
   const int first = cut.owner(u), last = cut.owner(u + q.units - 1);
   if (first == last) return;  // written by that block
-  const int row = h - kh * heads - hg * DEC_ROWS;
+  const int row = h - kh * heads - hg * A.per_item;
   // a piece is its block's second one when the item begins in that block
   auto piece = [&](int c) {
     return A.ws + ((size_t)(c * 2 + (cut.start(c) <= u ? 1 : 0)) * A.rows + row) * (DP + 2);
@@ -620,15 +725,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
 }
 
 int64_t attn_decode_ws(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
-  const int64_t rows = std::min<int64_t>(n_heads / std::max<int64_t>(n_kv_heads, 1), DEC_ROWS);
+  const int64_t rows = std::min<int64_t>(n_heads / std::max<int64_t>(n_kv_heads, 1), DEC_MAX_ROWS);
   return (int64_t)DEC_MAX_BLOCKS * 2 * rows * ((head_dim <= 64 ? 64 : 128) + 2) * 4;
 }
 
-template <int DP, bool E4M3>
+template <int DP, bool E4M3, int NB>
 static cudaError_t launch_decode_t(DecArgs A, cudaStream_t s) {
   static SmemOptIn opt_in;
-  auto kern = k_attn_decode<DP, E4M3>;
-  constexpr int smem = DecShape<DP, E4M3>::SMEM;
+  auto kern = k_attn_decode<DP, E4M3, NB>;
+  constexpr int smem = DecShape<DP, E4M3, NB>::SMEM;
   if (cudaError_t e = opt_in(kern, smem, true)) return e;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -636,18 +741,24 @@ static cudaError_t launch_decode_t(DecArgs A, cudaStream_t s) {
   A.blocks = std::min(std::max(sms, 1) * 2, DEC_MAX_BLOCKS);
   if (cudaError_t e = launch_pdl(kern, dim3(A.blocks), dim3(DEC_THREADS), smem, s, A)) return e;
   const int64_t joins = A.a.n_seq * ceil_div<int64_t>(A.a.n_heads, JOIN_HEADS);
-  return launch_pdl(k_attn_join<DP>, dim3((unsigned)joins), dim3(JOIN_THREADS), 0, s, A);
+  return launch_pdl(k_attn_join<DP, dec_tile(E4M3)>, dim3((unsigned)joins), dim3(JOIN_THREADS), 0, s, A);
+}
+
+template <int DP, bool E4M3>
+static cudaError_t launch_decode_heads(DecArgs A, cudaStream_t s) {
+  const int heads = A.a.n_heads / A.a.c.H;
+  A.per_item = heads <= 8 ? 8 : 16;  // more than 16 query heads on a key head: it is read again
+  A.groups = (heads + A.per_item - 1) / A.per_item;
+  A.rows = std::min(heads, A.per_item);
+  return heads <= 8 ? launch_decode_t<DP, E4M3, 1>(A, s) : launch_decode_t<DP, E4M3, 2>(A, s);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs &a, bool e4m3, float *ws, cudaStream_t s) {
   DecArgs A = {};
   A.a = a;
   A.ws = ws;
-  const int heads = a.n_heads / a.c.H;
-  A.groups = (heads + DEC_ROWS - 1) / DEC_ROWS;
-  A.rows = std::min(heads, DEC_ROWS);
-  if (a.c.D <= 64) return e4m3 ? launch_decode_t<64, true>(A, s) : launch_decode_t<64, false>(A, s);
-  return e4m3 ? launch_decode_t<128, true>(A, s) : launch_decode_t<128, false>(A, s);
+  if (a.c.D <= 64) return e4m3 ? launch_decode_heads<64, true>(A, s) : launch_decode_heads<64, false>(A, s);
+  return e4m3 ? launch_decode_heads<128, true>(A, s) : launch_decode_heads<128, false>(A, s);
 }
 
 }  // namespace bwta
