@@ -11,6 +11,7 @@ Bit planes are returned as int32 tensors holding the uint32 words
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 
@@ -564,21 +565,27 @@ def kv_layers(caches) -> KvLayers:
     return KvLayers([caches] if isinstance(caches, KvCache) else caches)
 
 
-class _on:
-    """Makes a device the current one for a call, where it is not already."""
-    __slots__ = ("dev", "was")
+_device_now = torch._C._cuda_getDevice
+_stream_now = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device):
-        self.dev = device.index
-        self.was = torch.cuda.current_device()
 
-    def __enter__(self):
-        if self.was != self.dev:
-            torch.cuda.set_device(self.dev)
+def _kv_call(name, device, *args):
+    """Call libbwta's `name` with these arguments and the current stream of `device`. The host's time
+    is most of a small call's, so nothing here builds stream or device objects."""
+    fn = getattr(_lib or _L(), name)
+    dev = device.index
+    if _device_now() == dev:
+        rc = fn(*args, _stream_now(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream_now(dev))
+    if rc != BWTA_OK:
+        raise BwtaError(name, rc)
 
-    def __exit__(self, *exc):
-        if self.was != self.dev:
-            torch.cuda.set_device(self.was)
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(name, *args):
+    return getattr(load_library(), name)(*args)
 
 
 def _ints(t, device):
@@ -598,8 +605,13 @@ def _status(t, device):
 
 def _kv_rows(t, width, device):
     """(pointer, row stride, rows) of rows of `width` values: [n, width] or [n, heads, dim]."""
-    assert t.device == device and t.dim() in (2, 3)
-    if t.dim() == 3:
+    n = t.dim()
+    assert t.device == device and n in (2, 3)
+    if t.is_contiguous():
+        rows = t.shape[0]
+        assert (t.shape[1] * t.shape[2] if n == 3 else t.shape[1]) == width
+        return t.data_ptr(), width, rows
+    if n == 3:
         assert t.shape[2] <= 1 or t.stride(2) == 1
         assert t.shape[1] <= 1 or t.stride(1) == t.shape[2]
         assert t.shape[1] * t.shape[2] == width
@@ -612,7 +624,6 @@ def bwta_kv_append(cache: KvCache, table: KvTable, k, v, slots=None, cu_q=None, 
     """New tokens' keys and values, fp32 or fp16 [rows, n_kv_heads * head_dim] (or three dimensions),
     into the pages. Without cu_q one row for each slot (or for each of `slots`); with it rows
     cu_q[s] .. cu_q[s+1] belong to sequence s and end at its kv_len."""
-    lib = _L()
     dev = cache.device
     assert table.device == dev and k.dtype == v.dtype and k.dtype in (torch.float16, torch.float32)
     width = cache.c.n_kv_heads * cache.c.head_dim
@@ -620,11 +631,9 @@ def bwta_kv_append(cache: KvCache, table: KvTable, k, v, slots=None, cu_q=None, 
     vp, ldv, nv = _kv_rows(v, width, dev)
     assert n == nv
     n_seq = _n_seq(table, slots, cu_q, n)
-    with _on(dev):
-        rc = lib.bwta_kv_append(cache.ref, table.ref, _ints(slots, dev), n_seq, _ints(cu_q, dev), n,
-                                kp, ldk, vp, ldv, int(k.dtype == torch.float32),
-                                _status(status, dev), _stream())
-    _check("bwta_kv_append", rc)
+    _kv_call("bwta_kv_append", dev, cache.ref, table.ref, _ints(slots, dev), n_seq, _ints(cu_q, dev), n,
+             kp, ldk, vp, ldv, int(k.dtype == torch.float32),
+             _status(status, dev))
 
 
 def _n_seq(table, slots, cu_q, rows):
@@ -638,7 +647,6 @@ def bwta_attn_decode_paged(q, cache: KvCache, table: KvTable, softmax_scale: flo
                            sinks: int = 0, slots=None, workspace=None, status=None, out=None):
     """Attention of one new token of each sequence over its pages. q fp16 [n_seq, n_heads, head_dim]
     -> out, the same shape. workspace: uint8 of decode_workspace() bytes (allocated when not given)."""
-    lib = _L()
     dev, D = cache.device, cache.c.head_dim
     assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
     n, heads = q.shape[0], q.shape[1]
@@ -651,19 +659,17 @@ def bwta_attn_decode_paged(q, cache: KvCache, table: KvTable, softmax_scale: flo
     if workspace is None:
         workspace = decode_workspace(heads, cache)
     assert workspace.device == dev and workspace.is_contiguous()
-    with _on(dev):
-        rc = lib.bwta_attn_decode_paged(cache.ref, table.ref, _ints(slots, dev), n_seq, qp, ldq,
-                                        heads, softmax_scale, window, sinks, op, ldo,
-                                        workspace.data_ptr(), workspace.nbytes,
-                                        _status(status, dev), _stream())
-    _check("bwta_attn_decode_paged", rc)
+    _kv_call("bwta_attn_decode_paged", dev, cache.ref, table.ref, _ints(slots, dev), n_seq, qp, ldq,
+             heads, softmax_scale, window, sinks, op, ldo,
+             workspace.data_ptr(), workspace.nbytes,
+             _status(status, dev))
     return out
 
 
 def decode_workspace(n_heads: int, cache: KvCache):
     """A workspace for bwta_attn_decode_paged; calls that may overlap in time need one each."""
     c = cache.c
-    n = load_library().bwta_attn_decode_workspace(n_heads, c.n_kv_heads, c.head_dim)
+    n = _workspace_bytes("bwta_attn_decode_workspace", n_heads, c.n_kv_heads, c.head_dim)
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
@@ -672,7 +678,6 @@ def bwta_attn_prompt_paged(q, cu_q, cache: KvCache, table: KvTable, softmax_scal
     """Attention of many new tokens of each sequence over its pages, which hold them already.
     q fp16 [rows, n_heads, head_dim], rows cu_q[s] .. cu_q[s+1] the newest of sequence s -> out, the
     same shape (rows past the last sequence are left as they are)."""
-    lib = _L()
     dev, D = cache.device, cache.c.head_dim
     assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
     n, heads = q.shape[0], q.shape[1]
@@ -682,60 +687,48 @@ def bwta_attn_prompt_paged(q, cu_q, cache: KvCache, table: KvTable, softmax_scal
         out = torch.empty((n, heads, D), dtype=torch.float16, device=dev)
     assert out.dtype == torch.float16 and out.shape == q.shape
     op, ldo, _ = _kv_rows(out, heads * D, dev)
-    with _on(dev):
-        rc = lib.bwta_attn_prompt_paged(cache.ref, table.ref, _ints(slots, dev), n_seq,
-                                        _ints(cu_q, dev), n, qp, ldq, heads, softmax_scale, window,
-                                        sinks, op, ldo, _status(status, dev), _stream())
-    _check("bwta_attn_prompt_paged", rc)
+    _kv_call("bwta_attn_prompt_paged", dev, cache.ref, table.ref, _ints(slots, dev), n_seq,
+             _ints(cu_q, dev), n, qp, ldq, heads, softmax_scale, window,
+             sinks, op, ldo, _status(status, dev))
     return out
 
 
 def bwta_kv_reserve(table: KvTable, page_size: int, slots, n_new, status=None):
     """Room for n_new[i] more tokens in slot slots[i]; raises kv_len."""
-    lib = _L()
     dev = table.device
     assert table.refcount is not None and slots.shape == n_new.shape
-    with _on(dev):
-        rc = lib.bwta_kv_reserve(table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
-                                 _ints(n_new, dev), slots.shape[0], _status(status, dev), _stream())
-    _check("bwta_kv_reserve", rc)
+    _kv_call("bwta_kv_reserve", dev, table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
+             _ints(n_new, dev), slots.shape[0], _status(status, dev))
 
 
 def bwta_kv_free(table: KvTable, page_size: int, slots, status=None):
     """Give up the slots' pages."""
-    lib = _L()
     dev = table.device
     assert table.refcount is not None
-    with _on(dev):
-        rc = lib.bwta_kv_free(table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
-                              slots.shape[0], _status(status, dev), _stream())
-    _check("bwta_kv_free", rc)
+    _kv_call("bwta_kv_free", dev, table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
+             slots.shape[0], _status(status, dev))
 
 
 def pages_workspace(num_pages: int, n: int, device="cuda"):
     """A workspace for the page calls: num_pages of the pool (fork, compact) and n list entries."""
-    return torch.empty(load_library().bwta_kv_pages_workspace(num_pages, n), dtype=torch.uint8,
+    return torch.empty(_workspace_bytes("bwta_kv_pages_workspace", num_pages, n), dtype=torch.uint8,
                        device=device)
 
 
 def bwta_kv_fork(caches, table: KvTable, src, dst, workspace=None, status=None):
     """Make slot dst[i] a copy of slot src[i], in all layers: full pages shared, the rest copied."""
-    lib = _L()
     l = kv_layers(caches)
     dev = l.device
     assert table.refcount is not None and table.refcount.shape[0] == l.num_pages
     assert src.shape == dst.shape and table.device == dev
     ws = pages_workspace(l.num_pages, src.shape[0], dev) if workspace is None else workspace
     assert ws.device == dev and ws.is_contiguous()
-    with _on(dev):
-        rc = lib.bwta_kv_fork(l.c, l.n, table.ref, _ints(src, dev), _ints(dst, dev), src.shape[0],
-                              ws.data_ptr(), ws.nbytes, _status(status, dev), _stream())
-    _check("bwta_kv_fork", rc)
+    _kv_call("bwta_kv_fork", dev, l.c, l.n, table.ref, _ints(src, dev), _ints(dst, dev), src.shape[0],
+             ws.data_ptr(), ws.nbytes, _status(status, dev))
 
 
 def bwta_kv_compact(caches, table: KvTable, workspace=None, status=None, out=None):
     """Move the pages in use to the front of the pool, in all layers. Returns int32 [1]: how many."""
-    lib = _L()
     l = kv_layers(caches)
     dev = l.device
     assert table.refcount is not None and table.refcount.shape[0] == l.num_pages
@@ -744,26 +737,21 @@ def bwta_kv_compact(caches, table: KvTable, workspace=None, status=None, out=Non
     assert ws.device == dev and ws.is_contiguous()
     if out is None:
         out = torch.empty(1, dtype=torch.int32, device=dev)
-    with _on(dev):
-        rc = lib.bwta_kv_compact(l.c, l.n, table.ref, _ints(out, dev), ws.data_ptr(), ws.nbytes,
-                                 _status(status, dev), _stream())
-    _check("bwta_kv_compact", rc)
+    _kv_call("bwta_kv_compact", dev, l.c, l.n, table.ref, _ints(out, dev), ws.data_ptr(), ws.nbytes,
+             _status(status, dev))
     return out
 
 
 def bwta_kv_copy_pages(src_caches, dst_caches, src_pages, dst_pages, workspace=None, status=None):
     """Copy page src_pages[i] of src to page dst_pages[i] of dst, in all layers."""
-    lib = _L()
     a, b = kv_layers(src_caches), kv_layers(dst_caches)
     dev = a.device
     assert b.device == dev and a.n == b.n and src_pages.shape == dst_pages.shape
     n = src_pages.shape[0]
     ws = pages_workspace(0, n, dev) if workspace is None else workspace
     assert ws.device == dev and ws.is_contiguous()
-    with _on(dev):
-        rc = lib.bwta_kv_copy_pages(a.c, b.c, a.n, _ints(src_pages, dev), _ints(dst_pages, dev), n,
-                                    ws.data_ptr(), ws.nbytes, _status(status, dev), _stream())
-    _check("bwta_kv_copy_pages", rc)
+    _kv_call("bwta_kv_copy_pages", dev, a.c, b.c, a.n, _ints(src_pages, dev), _ints(dst_pages, dev), n,
+             ws.data_ptr(), ws.nbytes, _status(status, dev))
 
 
 # ------------------------------------------------------------------ helpers

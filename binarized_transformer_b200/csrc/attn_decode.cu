@@ -54,15 +54,15 @@ struct DecShape {
   static constexpr int SUB = dec_tile(E4M3) / DEC_WARPS;  // tokens of one warp in a unit
   static constexpr int TILE = dec_tile(E4M3);
   static constexpr int ROW = DP * (E4M3 ? 1 : 2);      // bytes of a token's row in the ring
-  static constexpr int STAGES = DP == 64 ? 6 : 3;
+  static constexpr int BLOCKS = NB == 1 ? 3 : 2;  // on an SM
+  static constexpr int STAGES = (NB == 1 ? 2 : 3) * (DP == 64 ? 2 : 1);
   static constexpr int HALF = SUB * ROW;               // keys (or values) of a stage
   static constexpr int STAGE = 2 * HALF + (E4M3 ? 2 * SUB * 4 : 0);
   static constexpr int RING = DEC_WARPS * STAGES * STAGE;
   static constexpr int PART = (DP / 16 * NB * 4 + 4 * NB) * 32;  // floats of one warp's running values
-  static constexpr int PARTS = NB == 1 ? 3 : 1;        // kept so that two blocks fit an SM
-  static constexpr int SMEM = RING + PARTS * PART * 4;
-  static_assert(PARTS * PART * 4 >= (DEC_THREADS + 1 + DEC_WARPS) * 8, "the prefix sums share the place");
-  static_assert(2 * (SMEM + 1024) <= 233472, "two blocks on an SM");
+  static constexpr int SMEM = RING + PART * 4;
+  static_assert(PART * 4 >= (DEC_THREADS + 1 + DEC_WARPS) * 8, "the prefix sums share the place");
+  static_assert(BLOCKS * (SMEM + 1024) <= 233472, "shared memory of an SM");
 };
 
 struct DecArgs {
@@ -221,7 +221,7 @@ struct DecCursor {
 };
 
 template <int DP, bool E4M3, int NB>
-__global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A) {
+__global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k_attn_decode(const DecArgs A) {
   using S = DecShape<DP, E4M3, NB>;
   constexpr int SUB = S::SUB, TILE = S::TILE, MT = SUB / 16, KS = DP / 16, ROWS = 8 * NB;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -232,11 +232,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
   float *joint = reinterpret_cast<float *>(smem + S::RING);
   int64_t *before = reinterpret_cast<int64_t *>(joint), *sums = before + DEC_THREADS + 1;
 
-  pdl_trigger();
   if (D < DP)  // columns past D are never written: zero once
     for (int i = threadIdx.x * 16; i < S::RING; i += DEC_THREADS * 16)
       *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0, 0, 0, 0);
   pdl_wait();
+  pdl_trigger();  // after the wait: k_attn_join may then read the lengths before its own
   const int per = dec_scan<DEC_THREADS, TILE>(a, before, sums);  // its barriers cover the zeros
   const DecCut cut(before[DEC_THREADS] * items, A.blocks);
   if ((int)blockIdx.x >= cut.blocks) return;
@@ -598,21 +598,12 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
                 o[b][ks][x] = o[b][ks][x] * fa + p[(4 * NB + (b * KS + ks) * 4 + x) * 32 + lane] * fb;
           }
       };
-      if (S::PARTS == 3) {
-        if (warp > 0) give(joint + (warp - 1) * S::PART);
-        __syncthreads();
-        if (warp == 0)
 #pragma unroll 1
-          for (int x = 0; x < 3; ++x) take(joint + x * S::PART);
+      for (int x = 1; x < DEC_WARPS; ++x) {
+        if (warp == x) give(joint);
         __syncthreads();
-      } else {
-#pragma unroll 1
-        for (int x = 1; x < DEC_WARPS; ++x) {
-          if (warp == x) give(joint);
-          __syncthreads();
-          if (warp == 0) take(joint);
-          __syncthreads();
-        }
+        if (warp == 0) take(joint);
+        __syncthreads();
       }
       if (warp == 0) {
         const bool began = i >= at.unit;  // the item's first unit is this block's too
@@ -660,56 +651,105 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) k_attn_decode(const DecArgs A)
   if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
 }
 
-// The outputs of items that several blocks share, and of empty sequences. A warp
-// a query head, 4 columns a lane.
-template <int DP, int TILE>
+// The outputs of items that several blocks share, and of empty sequences: a warp a
+// query head, 4 columns a lane. WIDE, for calls of few items, each spread over many
+// blocks: a block a query head, its warps take the pieces in turn.
+template <int DP, int TILE, bool WIDE>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
   __shared__ int64_t before[JOIN_THREADS + 1], sums[JOIN_THREADS / 32];
+  __shared__ float part[WIDE ? JOIN_HEADS : 1][DP + 2];
   const AttnArgs &a = A.a;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int hb = (a.n_heads + JOIN_HEADS - 1) / JOIN_HEADS;
+  const int hb = WIDE ? a.n_heads : (a.n_heads + JOIN_HEADS - 1) / JOIN_HEADS;
   const int64_t s = blockIdx.x / hb;
-  const int h = (int)(blockIdx.x - s * hb) * JOIN_HEADS + warp;
+  const int hx = (int)(blockIdx.x - s * hb), h = WIDE ? hx : hx * JOIN_HEADS + warp;
   const int D = a.c.D, heads = a.n_heads / a.c.H, items = a.c.H * A.groups;
-  pdl_trigger();
-  pdl_wait();
+  // the table is as k_attn_decode found it; its pieces are what has to be waited for
   const int per = dec_scan<JOIN_THREADS, TILE>(a, before, sums);
-  if (h >= a.n_heads) return;
   const DecSeq q = dec_seq<TILE>(a, s);
+  const DecCut cut(before[JOIN_THREADS] * items, A.blocks);
+  int64_t u = 0;
+  int first = 0, last = 0, row = 0;
+  if (h < a.n_heads && q.units > 0) {
+    const int who = (int)(s / per), kh = h / heads, hg = (h - kh * heads) / A.per_item;
+    u = before[who] * items;
+    for (int64_t i = (int64_t)who * per; i < s; ++i) u += (int64_t)dec_seq<TILE>(a, i).units * items;
+    u += (int64_t)(kh * A.groups + hg) * q.units;
+    first = cut.owner(u);
+    last = cut.owner(u + q.units - 1);
+    row = h - kh * heads - hg * A.per_item;
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (h >= a.n_heads) return;
   uint16_t *out = a.out + s * a.ldo + (int64_t)h * D + lane * 4;
   if (q.units == 0) {
+    if (WIDE && warp > 0) return;
     if (q.bad && lane == 0 && h == 0) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
     if (lane * 4 < D) *reinterpret_cast<uint2 *>(out) = make_uint2(0, 0);
     return;
   }
-  const DecCut cut(before[JOIN_THREADS] * items, A.blocks);
-  const int who = (int)(s / per), kh = h / heads, hg = (h - kh * heads) / A.per_item;
-  int64_t u = before[who] * items;
-  for (int64_t i = (int64_t)who * per; i < s; ++i) u += (int64_t)dec_seq<TILE>(a, i).units * items;
-  u += (int64_t)(kh * A.groups + hg) * q.units;
-  const int first = cut.owner(u), last = cut.owner(u + q.units - 1);
   if (first == last) return;  // written by that block
-  const int row = h - kh * heads - hg * A.per_item;
   // a piece is its block's second one when the item begins in that block
   auto piece = [&](int c) {
     return A.ws + ((size_t)(c * 2 + (cut.start(c) <= u ? 1 : 0)) * A.rows + row) * (DP + 2);
   };
+  constexpr int BY = WIDE ? JOIN_HEADS : 1;
   float M = -INFINITY, L = 0.0f, y[4] = {0, 0, 0, 0};
-  for (int c = first + lane; c <= last; c += 32) M = fmaxf(M, piece(c)[DP]);
+  const bool col = lane * 4 < D;
+  for (int c0 = first + (WIDE ? warp : 0); c0 <= last; c0 += 32 * BY) {
+    // 32 pieces: a lane holds one's maximum and sum
+    const int c = c0 + lane * BY, n = min(32, (last - c0) / BY + 1);
+    float pm = -INFINITY, pl = 0.0f;
+    if (c <= last) {
+      const float2 ml = *reinterpret_cast<const float2 *>(piece(c) + DP);
+      pm = ml.x;
+      pl = ml.y;
+    }
+    float top = pm;
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(FULL, M, d));
-#pragma unroll 4
-  for (int c = first; c <= last; ++c) {
-    const float *p = piece(c);
-    const float f = p[DP] == -INFINITY ? 0.0f : exp2_fast(p[DP] - M);
-    L += p[DP + 1] * f;
-    if (lane * 4 < D) {
-      const float2 v0 = *reinterpret_cast<const float2 *>(p + lane * 4);
-      const float2 v1 = *reinterpret_cast<const float2 *>(p + lane * 4 + 2);
-      y[0] += v0.x * f;
-      y[1] += v0.y * f;
-      y[2] += v1.x * f;
-      y[3] += v1.y * f;
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+    const float mn = fmaxf(M, top);
+    const float old = M == -INFINITY ? 0.0f : exp2_fast(M - mn);
+    const float f = pm == -INFINITY ? 0.0f : exp2_fast(pm - mn);
+    M = mn;
+    L = L * old + pl * f;  // this lane's share
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] *= old;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float fi = __shfl_sync(FULL, f, i);
+      const float *p = piece(c0 + i * BY);
+      if (col) {
+        const float2 v0 = *reinterpret_cast<const float2 *>(p + lane * 4);
+        const float2 v1 = *reinterpret_cast<const float2 *>(p + lane * 4 + 2);
+        y[0] += v0.x * fi;
+        y[1] += v0.y * fi;
+        y[2] += v1.x * fi;
+        y[3] += v1.y * fi;
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) L += __shfl_xor_sync(FULL, L, d);
+  if (WIDE) {
+    if (lane == 0) {
+      part[warp][DP] = M;
+      part[warp][DP + 1] = L;
+    }
+    if (col)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[warp][lane * 4 + e] = y[e];
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 0; w < JOIN_HEADS; ++w) M = fmaxf(M, part[w][DP]);
+    L = y[0] = y[1] = y[2] = y[3] = 0.0f;
+    for (int w = 0; w < JOIN_HEADS; ++w) {
+      const float f = part[w][DP] == -INFINITY ? 0.0f : exp2_fast(part[w][DP] - M);
+      L += part[w][DP + 1] * f;
+      if (col)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += part[w][lane * 4 + e] * f;
     }
   }
   bool finite = true;
@@ -718,7 +758,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
     y[e] /= L;
     finite &= y[e] - y[e] == 0.0f;
   }
-  if (lane * 4 < D) {
+  if (col) {
     *reinterpret_cast<uint2 *>(out) = make_uint2(half2_bits(y[0], y[1]), half2_bits(y[2], y[3]));
     if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
   }
@@ -738,10 +778,13 @@ static cudaError_t launch_decode_t(DecArgs A, cudaStream_t s) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  A.blocks = std::min(std::max(sms, 1) * 2, DEC_MAX_BLOCKS);
+  A.blocks = std::min(std::max(sms, 1) * DecShape<DP, E4M3, NB>::BLOCKS, DEC_MAX_BLOCKS);
   if (cudaError_t e = launch_pdl(kern, dim3(A.blocks), dim3(DEC_THREADS), smem, s, A)) return e;
-  const int64_t joins = A.a.n_seq * ceil_div<int64_t>(A.a.n_heads, JOIN_HEADS);
-  return launch_pdl(k_attn_join<DP, dec_tile(E4M3)>, dim3((unsigned)joins), dim3(JOIN_THREADS), 0, s, A);
+  // An item of a call with few of them is cut into many pieces.
+  const bool wide = A.a.n_seq * A.a.c.H * A.groups * 16 <= A.blocks;
+  const int64_t joins = A.a.n_seq * (wide ? A.a.n_heads : ceil_div<int64_t>(A.a.n_heads, JOIN_HEADS));
+  return launch_pdl(wide ? k_attn_join<DP, dec_tile(E4M3), true> : k_attn_join<DP, dec_tile(E4M3), false>,
+                    dim3((unsigned)joins), dim3(JOIN_THREADS), 0, s, A);
 }
 
 template <int DP, bool E4M3>
