@@ -67,28 +67,34 @@ __device__ __forceinline__ bool store_row4(float4 x, uint8_t *base, float *scale
   return !live || (!nan && top4 < 65520.0f);
 }
 
-template <int LPR, bool F32, bool E4M3>
+// A group of LPR lanes takes HB heads of one token at a time: where they go is looked
+// up once, and all their loads are under way before the first is used.
+template <int LPR, int HB, bool F32, bool E4M3>
 __global__ void __launch_bounds__(AP_THREADS) k_kv_append(const KvAppendArgs a) {
   pdl_trigger();
   pdl_wait();
   const int sub = threadIdx.x % LPR, d = sub * 4;
   const int64_t group = ((int64_t)blockIdx.x * AP_THREADS + threadIdx.x) / LPR;
   const int64_t groups = (int64_t)gridDim.x * AP_THREADS / LPR;
-  const int64_t rows = (a.cu_q ? (int64_t)min((int64_t)a.cu_q[a.n_seq], a.total_q) : a.total_q) * a.c.H;
+  const int hb = (a.c.H + HB - 1) / HB;
+  const int64_t work = (a.cu_q ? (int64_t)min((int64_t)a.cu_q[a.n_seq], a.total_q) : a.total_q) * hb;
   bool bad = false, finite = true;
-  const int64_t rounds = ceil_div<int64_t>(rows, groups);
+  const int64_t rounds = ceil_div<int64_t>(work, groups);
   for (int64_t i = 0; i < rounds; ++i) {  // every lane of a warp takes every round: shuffles inside
     const int64_t r = i * groups + group;
-    const bool in = r < rows;
-    const int64_t tok = in ? r / a.c.H : 0;
-    const int h = in ? (int)(r - tok * a.c.H) : 0;
-    const bool col = in && d < a.c.D;
-    float4 xk = make_float4(0, 0, 0, 0), xv = xk;
-    if (col) {
-      xk = load_row4<F32>(a.k, tok * a.ldk + (int64_t)h * a.c.D + d);
-      xv = load_row4<F32>(a.v, tok * a.ldv + (int64_t)h * a.c.D + d);
+    const bool in = r < work;
+    const int64_t tok = in ? r / hb : 0;
+    const int h0 = in ? (int)(r - tok * hb) * HB : 0;
+    float4 xk[HB], xv[HB];
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+      xk[j] = xv[j] = make_float4(0, 0, 0, 0);
+      if (in && h0 + j < a.c.H && d < a.c.D) {
+        xk[j] = load_row4<F32>(a.k, tok * a.ldk + (int64_t)(h0 + j) * a.c.D + d);
+        xv[j] = load_row4<F32>(a.v, tok * a.ldv + (int64_t)(h0 + j) * a.c.D + d);
+      }
     }
-    bool live = col;
+    bool live = in && d < a.c.D;
     int64_t at = 0, sat = 0;
     if (in) {
       const int64_t s = a.cu_q ? kv_find_seq(a.cu_q, a.n_seq, tok) : tok;
@@ -102,36 +108,49 @@ __global__ void __launch_bounds__(AP_THREADS) k_kv_append(const KvAppendArgs a) 
         bad = true;
         live = false;
       } else {
-        const int64_t row = (int64_t)h * a.c.ps + (pos - idx * a.c.ps);
+        const int64_t row = (int64_t)h0 * a.c.ps + (pos - idx * a.c.ps);
         at = (int64_t)page * a.c.page_stride + row * a.c.D + d;
         sat = (int64_t)page * a.c.scale_stride + row;
       }
     }
-    finite &= store_row4<LPR, E4M3>(xk, const_cast<uint8_t *>(a.c.k), const_cast<float *>(a.c.ks), at, sat, sub, live);
-    finite &= store_row4<LPR, E4M3>(xv, const_cast<uint8_t *>(a.c.v), const_cast<float *>(a.c.vs), at, sat, sub, live);
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+      const bool on = live && h0 + j < a.c.H;
+      const int64_t to = at + (int64_t)j * a.c.ps * a.c.D, sto = sat + (int64_t)j * a.c.ps;
+      finite &= store_row4<LPR, E4M3>(xk[j], const_cast<uint8_t *>(a.c.k), const_cast<float *>(a.c.ks), to, sto, sub, on);
+      finite &= store_row4<LPR, E4M3>(xv[j], const_cast<uint8_t *>(a.c.v), const_cast<float *>(a.c.vs), to, sto, sub, on);
+    }
   }
   if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
   if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
 }
 
-template <int LPR>
-static cudaError_t launch_append_t(const KvAppendArgs &a, cudaStream_t s) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t blocks = std::min<int64_t>(ceil_div<int64_t>(a.total_q * a.c.H * LPR, AP_THREADS),
-                                           (int64_t)std::max(sms, 1) * 8);
+template <int LPR, int HB>
+static cudaError_t launch_append_t(const KvAppendArgs &a, int sms, cudaStream_t s) {
+  const int64_t blocks = std::min<int64_t>(
+      ceil_div<int64_t>(a.total_q * ceil_div(a.c.H, HB) * LPR, AP_THREADS), (int64_t)sms * 8);
   auto go = [&](auto kern) {
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(AP_THREADS), 0, s, a);
   };
-  if (a.f32) return a.e4m3 ? go(k_kv_append<LPR, true, true>) : go(k_kv_append<LPR, true, false>);
-  return a.e4m3 ? go(k_kv_append<LPR, false, true>) : go(k_kv_append<LPR, false, false>);
+  if (a.f32) return a.e4m3 ? go(k_kv_append<LPR, HB, true, true>) : go(k_kv_append<LPR, HB, true, false>);
+  return a.e4m3 ? go(k_kv_append<LPR, HB, false, true>) : go(k_kv_append<LPR, HB, false, false>);
+}
+
+template <int LPR>
+static cudaError_t launch_append_rows(const KvAppendArgs &a, cudaStream_t s) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  sms = std::max(sms, 1);
+  // Several heads a group once every SM has its warps: below, one head each is the shorter way.
+  const bool many = a.total_q * a.c.H * LPR >= (int64_t)sms * 2048 * 4;
+  return many ? launch_append_t<LPR, 4>(a, sms, s) : launch_append_t<LPR, 1>(a, sms, s);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s) {
-  if (a.c.D <= 32) return launch_append_t<8>(a, s);
-  if (a.c.D <= 64) return launch_append_t<16>(a, s);
-  return launch_append_t<32>(a, s);
+  if (a.c.D <= 32) return launch_append_rows<8>(a, s);
+  if (a.c.D <= 64) return launch_append_rows<16>(a, s);
+  return launch_append_rows<32>(a, s);
 }
 
 }  // namespace bwta
