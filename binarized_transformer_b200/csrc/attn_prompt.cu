@@ -49,6 +49,7 @@ struct PrWarps {
 };
 constexpr int PR_LAG = 2;           // key or value tiles whose copies are in flight
 constexpr int PR_HALF = 64;         // keys of one product (scores and weights)
+constexpr int PR_MIN_STEPS = 2;     // key tiles that are worth a block of their own
 constexpr float PR_SLACK = 8.0f;    // how far scores may pass the reference (log2)
 template <int DP, bool E4M3>
 struct PrShape {
@@ -64,6 +65,7 @@ struct PrShape {
 struct PrArgs {
   AttnArgs a;
   int group, R;      // query heads of a key head, tokens of a tile
+  int split;         // blocks (a cluster) that share the key tiles of a pair
 };
 
 struct PrItem {
@@ -72,7 +74,10 @@ struct PrItem {
   int32_t cnt[2];      // tokens of each tile
   int32_t pmin[2];     // position of a tile's first token (may be negative)
   int32_t last[2], first[2], sink[2];  // its visible key tiles: [0, sink) and [first, last]; last < 0: none
-  int32_t u_sink, u_first, steps;      // the walk: [0, u_sink), then from u_first on
+  // this block's share of the walk over all of them: step j is tile j + j0 below u_sink
+  // (tiles among the sinks), j + u_first from there on
+  int32_t u_sink, u_first, j0, steps;
+  int32_t parts;       // blocks that have one
   int32_t lo, hi;      // tokens that some row sees: [lo, hi] and those below the sinks
   bool live;
 };
@@ -111,7 +116,7 @@ __device__ __forceinline__ bool pr_wait(PrBars *b, uint64_t *bar, uint32_t parit
 }
 
 __device__ __forceinline__ int pr_tile(const PrItem &it, int j) {
-  return j < it.u_sink ? j : it.u_first + j - it.u_sink;
+  return j + (j < it.u_sink ? it.j0 : it.u_first);
 }
 __device__ __forceinline__ bool pr_active(const PrItem &it, int a, int t) {
   return t <= it.last[a] && (t >= it.first[a] || t < it.sink[a]);
@@ -132,7 +137,7 @@ __device__ __forceinline__ void regs_dec() {
 __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
   const AttnArgs &a = A.a;
   const int lane = threadIdx.x % 32;
-  const int64_t at = blockIdx.x, H = a.c.H, two = 2 * A.R;
+  const int64_t at = blockIdx.x / A.split, H = a.c.H, two = 2 * A.R;
   int64_t before = 0;
   it.live = false;
   for (int64_t s0 = 0; s0 < a.n_seq; s0 += 32) {
@@ -164,7 +169,8 @@ __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
       if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
       it.head = (int32_t)head;
       it.row0 = c0 + pair * two;
-      it.steps = 0;
+      it.j0 = it.steps = 0;
+      it.parts = 1;
       int64_t pmax_all = -1, pmin_all = 0;
       int32_t u_last = -1, u_first = 0x7fffffff, u_sink = 0;
       for (int i = 0; i < 2; ++i) {
@@ -187,9 +193,13 @@ __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
         u_sink = max(u_sink, it.sink[i]);
       }
       if (u_last >= 0) {
-        it.u_sink = min(u_sink, u_first);
-        it.u_first = u_first;
-        it.steps = it.u_sink + u_last - u_first + 1;
+        u_sink = min(u_sink, u_first);
+        const int all = u_sink + u_last - u_first + 1, rank = blockIdx.x % A.split;
+        it.parts = max(1, min(A.split, all / PR_MIN_STEPS));
+        it.j0 = rank < it.parts ? (int)((int64_t)all * rank / it.parts) : 0;
+        it.steps = rank < it.parts ? (int)((int64_t)all * (rank + 1) / it.parts) - it.j0 : 0;
+        it.u_sink = u_sink - it.j0;
+        it.u_first = u_first - it.u_sink;
         it.lo = (int32_t)(a.window ? max((int64_t)0, pmin_all - a.window + 1) : 0);
         it.hi = (int32_t)pmax_all;
       }
@@ -197,6 +207,31 @@ __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
     }
     return;
   }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What lies at shared-memory address `at` of block `rank` of the cluster.
+__device__ __forceinline__ float2 cluster_ld2(uint32_t at, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
 }
 
 // Eight E4M3 bytes as halves times their row's scale (both exact in fp16).
@@ -410,15 +445,34 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       }
       // output
       bool finite = true;
-      if (it.last[w] >= 0 && ok) ok = __all_sync(FULL, pr_wait(bars, &bars->o_done[w], 0));
-      if (ok) {
+      // (the shared memory of keys and values is free once both tiles' products are done)
+      if (steps > 0 && ok)
+        ok = __all_sync(FULL, pr_wait(bars, &bars->o_done[w], 0) && pr_wait(bars, &bars->o_done[1 - w], 0));
+      if (ok && it.parts > 1 && steps > 0) {
+        // a share: for the cluster to add up
+        tc_fence_after();
+        float *part = reinterpret_cast<float *>(base + 2 * S::TILE) + (w * PR_T + r) * DP;
+#pragma unroll 1
+        for (int c = 0; c * 32 < D; ++c) {
+          uint32_t o[32];
+          if (halves > 0) {
+            tmem_ld32(to + c * 32, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(part + (((c * 8 + i) ^ r) % (DP / 4)) * 4) =
+                halves > 0 ? make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]) : make_uint4(0, 0, 0, 0);
+        }
+        *reinterpret_cast<float2 *>(base + (w * PR_T + r) * 8) = make_float2(m, l);
+      } else if (ok && blockIdx.x % A.split == 0) {
         tc_fence_after();
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a row that sees nothing: zeros
         // through shared memory (Q has been read), so that rows are written whole
 #pragma unroll 1
         for (int c = 0; c * 32 < D; ++c) {
           uint32_t o[32];
-          if (it.last[w] >= 0) {
+          if (halves > 0) {
             tmem_ld32(to + c * 32, o);
             tmem_wait_ld();
           }
@@ -647,8 +701,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       const int last = __shfl_sync(FULL, it.last[w], 0), first = __shfl_sync(FULL, it.first[w], 0);
       const int sink = __shfl_sync(FULL, it.sink[w], 0);
       const int u_sink = __shfl_sync(FULL, it.u_sink, 0), u_first = __shfl_sync(FULL, it.u_first, 0);
+      const int j0 = __shfl_sync(FULL, it.j0, 0);
       auto active = [&](int j) {
-        const int t = j < u_sink ? j : u_first + j - u_sink;
+        const int t = j + (j < u_sink ? j0 : u_first);
         return t <= last && (t >= first || t < sink);
       };
       auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, pr_wait(bars, bar, parity)); };
@@ -727,6 +782,51 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
 
   tc_fence_before();
   __syncthreads();
+  if (A.split > 1) {
+    // Shares of one pair: every block adds up some of its rows, o = sum_k o_k f_k / sum_k l_k f_k
+    // with f_k = 2^(m_k - max m), reading the others' shared memory.
+    cluster_sync();
+    const int parts = it.parts, rank = blockIdx.x % A.split;
+    if (it.live && parts > 1 && rank < parts && warp >= W::SOFTMAX0) {
+      bool finite = true;
+      const uint32_t ml0 = smem_addr(base), o0 = smem_addr(base + 2 * S::TILE);
+      for (int i = (warp - W::SOFTMAX0) * parts + rank; i < 2 * PR_T; i += 8 * parts) {
+        const int w = i / PR_T, r = i % PR_T;
+        if (r >= it.cnt[w] * A.group) continue;
+        float M = -INFINITY, L = 0.0f;
+        float4 y = make_float4(0, 0, 0, 0);
+        for (int k = 0; k < parts; ++k) M = fmaxf(M, cluster_ld2(ml0 + i * 8, k).x);
+        for (int k = 0; k < parts; ++k) {
+          const float2 ml = cluster_ld2(ml0 + i * 8, k);
+          const float f = ml.x == -INFINITY ? 0.0f : pr_exp2(ml.x - M);
+          L += ml.y * f;
+          const float4 x = cluster_ld4(o0 + (i * DP + ((lane ^ r) % (DP / 4)) * 4) * 4, k);
+          y.x += x.x * f;
+          y.y += x.y * f;
+          y.z += x.z * f;
+          y.w += x.w * f;
+        }
+        if (lane * 4 < D) {
+          const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+          float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[e] = inv == 0.0f ? 0.0f : z[e] * inv;
+            finite &= z[e] - z[e] == 0.0f;
+          }
+          const __half2 a2 = __floats2half2_rn(z[0], z[1]), b2 = __floats2half2_rn(z[2], z[3]);
+          const int tok = r / A.group;
+          uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R + tok) * a.ldo +
+                          ((int64_t)it.head * A.group + (r - tok * A.group)) * D;
+          *reinterpret_cast<uint2 *>(out + lane * 4) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&a2), *reinterpret_cast<const uint32_t *>(&b2));
+        }
+      }
+      if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
+    }
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its shares are read
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -745,7 +845,8 @@ static cudaError_t launch_prompt_t(const PrArgs &A, int64_t blocks, cudaStream_t
   static SmemOptIn opt_in;
   auto kern = k_attn_prompt<DP, E4M3>;
   if (cudaError_t e = opt_in(kern, PrShape<DP, E4M3>::SMEM)) return e;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PrWarps<E4M3>::THREADS), PrShape<DP, E4M3>::SMEM, s, A);
+  return launch_pdl_cluster(kern, dim3((unsigned)(blocks * A.split)), (unsigned)A.split, dim3(PrWarps<E4M3>::THREADS),
+                            PrShape<DP, E4M3>::SMEM, s, A);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
@@ -754,6 +855,17 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
   A.group = a.n_heads / a.c.H;
   A.R = PR_T / A.group;
   const int64_t blocks = attn_prompt_blocks(a.n_seq, a.total_q, a.n_heads, a.c.H);
+  // Few pairs leave SMs idle: up to 8 blocks then share the keys of each.
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // (As many as the longest walk that the table allows has shares for; measured: 3 rows
+  // over 8000 tokens 129 -> 25 us, while shares of nothing cost 1.4 us.)
+  int64_t tiles = ceil_div<int64_t>((int64_t)a.r.max_pages * a.c.ps, PR_T);
+  if (a.window)
+    tiles = std::min(tiles, (a.window + 2 * A.R) / PR_T + 2 + std::min(tiles, ceil_div<int64_t>(a.sinks, PR_T)));
+  A.split = 1;
+  while (A.split < 8 && blocks * A.split * 2 <= sms && tiles >= 2 * PR_MIN_STEPS * A.split) A.split *= 2;
   if (a.c.D <= 64)
     return e4m3 ? launch_prompt_t<64, true>(A, blocks, s) : launch_prompt_t<64, false>(A, blocks, s);
   return e4m3 ? launch_prompt_t<128, true>(A, blocks, s) : launch_prompt_t<128, false>(A, blocks, s);

@@ -119,27 +119,38 @@ __device__ __forceinline__ void pdl_trigger() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 #ifndef __CUDACC_RTC__
-// Launch `kern` on `s` with programmatic stream serialization allowed.
+// Launch `kern` on `s` with programmatic stream serialization allowed, in clusters
+// of `cluster` consecutive blocks (1: no clusters).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                       Args &&...args) {
+cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, unsigned cluster, dim3 block,
+                               size_t smem, cudaStream_t s, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-#ifdef BWTA_NO_PDL
-  cfg.numAttrs = 0;  // build-time option: plain stream-ordered launches
-#else
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+#ifndef BWTA_NO_PDL  // build-time option: plain stream-ordered launches
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
 #endif
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                       Args &&...args) {
+  return launch_pdl_cluster(kern, grid, 1, block, smem, s, static_cast<Args &&>(args)...);
 }
 #endif
 

@@ -211,6 +211,29 @@ def test_prompt(H, G, D, ps, lens, news, window, sinks, e4m3):
     b.check(q, out, news, D ** -0.5, window, sinks, rows=24)
 
 
+@pytest.mark.parametrize("H,G,D,ps,lens,news,window,sinks", [
+    (1, 1, 64, 16, [5000], [3], 0, 0),
+    (2, 8, 128, 32, [3000, 9, 700], [5, 9, 1], 0, 0),
+    (1, 4, 128, 64, [6000], [70], 2000, 300),
+    (1, 3, 40, 48, [2000, 1], [50, 1], 0, 0),
+    (4, 2, 96, 16, [513, 0, 1500], [130, 0, 200], 900, 1),
+    (1, 1, 128, 16, [1030], [300], 0, 0),
+    (1, 16, 80, 128, [4000], [17], 100, 2000),
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_prompt_of_few_rows(H, G, D, ps, lens, news, window, sinks, e4m3):
+    """Few rows over long caches: the keys of a tile are shared out and the parts added up."""
+    b = Batch(bt, lens, ps, H, D, e4m3, seed=len(lens) + D)
+    q = b.queries(sum(news), H * G, size=2.0)
+    status = bt.new_status()
+    args = (torch.from_numpy(q).cuda(), offsets(news), b.cache, b.table, D ** -0.5, window, sinks)
+    out = bt.bwta_attn_prompt_paged(*args, slots=b.slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    b.check(q, out, news, D ** -0.5, window, sinks, rows=24)
+    assert torch.equal(out, bt.bwta_attn_prompt_paged(*args, slots=b.slots))
+
+
 def test_prompt_rows_before_the_first_token_are_zero():
     b = Batch(bt, [5, 0], 16, 1, 64)
     q = torch.from_numpy(b.queries(12, 2)).cuda()
