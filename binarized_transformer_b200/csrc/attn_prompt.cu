@@ -42,6 +42,10 @@ struct PrWarps {
   static constexpr int LOAD = E4M3 ? 8 : 4;
   static constexpr int SOFTMAX0 = 4 + LOAD;  // the first softmax warp
   static constexpr int THREADS = (4 + LOAD + 8) * 32;
+  // The issuing warps' loop over halves: with the converting warps beside them the shorter
+  // code is faster (windowed chunk 543 -> 515 us), without them the longer (2 x 8192 tokens
+  // 1246 -> 1210 us).
+  static constexpr int MMA_UNROLL = E4M3 ? 1 : 2;
   // Registers by role; launched with 128 (96) a thread, so 4 x 128 (5 x 96) in all.
   static constexpr int REG_MMA = E4M3 ? 56 : 104, REG_LOAD = E4M3 ? 72 : 104;
   static constexpr int REG_SOFTMAX = E4M3 ? 136 : 152;
@@ -236,13 +240,17 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t at, int rank) {
 
 // Eight E4M3 bytes as halves times their row's scale (both exact in fp16).
 __device__ __forceinline__ uint4 pr_convert(uint2 b, uint32_t scale2) {
-  auto two = [&](uint32_t x) {
-    uint32_t h, r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(scale2));
-    return r;
+  auto four = [&](uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 a, b;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 a, l;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\t"
+        "mul.rn.f16x2 %0, a, %3;\n\tmul.rn.f16x2 %1, b, %3;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x), "r"(scale2));
   };
-  return make_uint4(two(b.x & 0xffffu), two(b.x >> 16), two(b.y & 0xffffu), two(b.y >> 16));
+  uint4 v;
+  four(b.x, v.x, v.y);
+  four(b.y, v.z, v.w);
+  return v;
 }
 
 // The lowest n bits.
@@ -521,10 +529,23 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       uint32_t rows;
     };
     auto token = [&](int j, int gi) { return pr_tile(it, j) * PR_T + (int)(w2 * GROUPS + gi) * 16; };
+    // tok / ps, both multiples of 16: the quotient of a multiplication is right or 1 short
+    const uint32_t ps16 = a.c.ps / 16, by_ps = 0xffffffffu / ps16;
+    const int32_t *row_of_pages = a.r.pages + (int64_t)it.slot * a.r.ld;
+    auto split = [&](int tok, int &in) -> int {
+      uint32_t n = __umulhi((uint32_t)tok / 16, by_ps), r = (uint32_t)tok / 16 - n * ps16;
+      if (r >= ps16) {
+        ++n;
+        r -= ps16;
+      }
+      in = (int)r * 16;
+      return (int)n;
+    };
     // the page's number is fetched a tile ahead
     auto page_of = [&](int j, int gi) -> int32_t {
       const int tok = token(j, gi);
-      return j < steps && tok <= it.hi ? a.r.pages[(int64_t)it.slot * a.r.ld + tok / a.c.ps] : -1;
+      int in;
+      return j < steps && tok <= it.hi ? row_of_pages[split(tok, in)] : -1;
     };
     auto place = [&](int j, int gi, int32_t page) -> Place {
       const int tok = token(j, gi);
@@ -544,7 +565,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         p.rows = 0;
         return p;
       }
-      const int64_t row = (int64_t)it.head * a.c.ps + tok % a.c.ps;
+      int in;
+      split(tok, in);
+      const int64_t row = (int64_t)it.head * a.c.ps + in;
       p.at = (int64_t)page * a.c.page_stride + row * D;
       p.sat = (int64_t)page * a.c.scale_stride + row;
       return p;
@@ -561,12 +584,14 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
     };
     bool ok = true;
     if (!E4M3) {
-      Place pl[2];
-      int32_t page[2] = {page_of(0, 0), page_of(0, 1)};
+      Place pl[GROUPS];
+      int32_t page[GROUPS];
+#pragma unroll
+      for (int gi = 0; gi < GROUPS; ++gi) page[gi] = page_of(0, gi);
       for (int u = 0; u < n && ok; ++u) {  // keys and values of a tile in turn
         if (!(u & 1)) {
 #pragma unroll
-          for (int gi = 0; gi < 2; ++gi) {
+          for (int gi = 0; gi < GROUPS; ++gi) {
             pl[gi] = place(u / 2, gi, page[gi]);
             page[gi] = page_of(u / 2 + 1, gi);
           }
@@ -577,7 +602,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         const uint32_t st = smem_addr(slot_of(u));
         const uint16_t *kv = reinterpret_cast<const uint16_t *>(u & 1 ? a.c.v : a.c.k);
 #pragma unroll
-        for (int gi = 0; gi < 2; ++gi)
+        for (int gi = 0; gi < GROUPS; ++gi)
 #pragma unroll
           for (int i = 0; i < ITER; ++i) {
             const int p = i * 32 + lane;
@@ -609,17 +634,14 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         const Place &p = pl;
         rows[q] = p.rows;
         ++fetched[q];
-        if (lane == 0) {
-          uint64_t *bar = &bars->raw[w2][q];
-          if (p.rows) {
-            const uint8_t *kv = (q == 0 ? a.c.k : a.c.v) + p.at;
-            const float *sc = (q == 0 ? a.c.ks : a.c.vs) + p.sat;
-            mbar_arrive_expect_tx(bar, 16 * D + 64);
-            bulk_load(raw + q * S::RAW, kv, 16 * D, bar);
-            bulk_load(raw + q * S::RAW + 16 * DP, sc, 64, bar);
-          } else {
-            mbar_arrive(bar);
-          }
+        uint64_t *bar = &bars->raw[w2][q];
+        if (p.rows) {
+          const uint32_t on = lane == 0;
+          mbar_arrive_expect_tx_if(on, bar, 16 * D + 64);
+          bulk_load_if(on, raw + q * S::RAW, (q == 0 ? a.c.k : a.c.v) + p.at, 16 * D, bar);
+          bulk_load_if(on, raw + q * S::RAW + 16 * DP, (q == 0 ? a.c.ks : a.c.vs) + p.sat, 64, bar);
+        } else if (lane == 0) {
+          mbar_arrive(bar);
         }
       };
       auto places = [&](int j) {
@@ -752,7 +774,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         const uint64_t vb = ring_mn + (uint64_t)(sv * (S::TILE >> 4));
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll W::MMA_UNROLL
         for (int h = 0; h < 2; ++h) {
           if (go) {
             ok = ok && ready(&bars->p_ready[w][h], p_phase);

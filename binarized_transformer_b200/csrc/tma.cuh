@@ -107,13 +107,23 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
       : "memory");
 }
 
+// Forms that a whole warp executes in step and one lane (on != 0) carries out.
+__device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t on, uint64_t *bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+      "r"(bytes), "r"(on)
+      : "memory");
+}
 // Bulk copy of consecutive bytes global -> shared, completion signalled on `bar`:
 // both addresses and the size multiples of 16.
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+__device__ __forceinline__ void bulk_load_if(uint32_t on, void *dst, const void *src, uint32_t bytes,
+                                             uint64_t *bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %4, 0;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(
           smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "r"(on)
       : "memory");
 }
 
