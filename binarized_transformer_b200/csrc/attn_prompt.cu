@@ -24,8 +24,8 @@
 // 64 values, 128-byte swizzle, one after another for each 64 of D): K is read
 // along D, V across it (MN-major).
 //
-// Rows of the cache that no row of the block sees are never read: zeros stand in
-// their place (a weight of 0 times a NaN would be one). Every wait is bounded; on a
+// Rows of the cache that no row of the block sees are zeros in shared memory (a weight
+// of 0 times a NaN would be one). Every wait is bounded; on a
 // timeout the block flags it, lets its copies and MMAs finish, frees TMEM and returns.
 #include <algorithm>
 

@@ -414,6 +414,7 @@ typedef struct bwta_kv_table {
  *           (total_q must be n_seq). Rows at and past cu_q[n_seq] are not read.
  *  k, v     rows of n_kv_heads * head_dim fp16 or fp32 values (row_type), ldk and
  *           ldv elements apart; 16-byte aligned, strides multiples of 16 bytes
+ *  The slots are distinct: of rows that go to the same place, parts of each may stay.
  *  A token whose position is negative, past the row of pages or on a page
  *  outside the pool is left out (BAD_PAGE). NONFINITE: a value that fp16 cannot
  *  hold; an fp16 cache then holds what the conversion gives (Inf or NaN), the

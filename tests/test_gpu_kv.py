@@ -269,6 +269,45 @@ def test_large_scores_and_equal_scores():
         b.check(zero, o, [1, 1], 1.0)
 
 
+@pytest.mark.parametrize("D,slope", [(64, 0.05), (128, 0.02), (64, -0.05), (40, 0.5)])
+def test_scores_that_keep_rising(D, slope):
+    """Each key scores above (or below) the one before: the running maximum moves all the way."""
+    t, n = 1300, 400
+    b = Batch(bt, [t], 16, 1, D)
+    k = np.repeat((np.arange(t) * slope % 64.0)[:, None], D, 1) if abs(slope) > 0.1 else \
+        np.repeat((np.arange(t) * slope)[:, None], D, 1)
+    b.k[0] = k[None].astype(np.float16).astype(np.float64)
+    for i in range(-(-t // 16)):
+        m = min(16, t - i * 16)
+        page = b.table.pages[b.slot_of[0], i].item()
+        b.cache.k[page, 0, :m] = torch.from_numpy(b.k[0][0, i * 16:i * 16 + m].astype(np.float16)).cuda()
+    q = np.abs(b.queries(n, 2)) + np.float16(0.5)
+    qt = torch.from_numpy(q).cuda()
+    status = bt.new_status()
+    out = bt.bwta_attn_prompt_paged(qt, cu([0, n]), b.cache, b.table, 0.125, slots=b.slots, status=status)
+    b.check(q, out, [n], 0.125, rows=40)
+    out = bt.bwta_attn_decode_paged(qt[-1:], b.cache, b.table, 0.125, slots=b.slots, status=status)
+    b.check(q[-1:], out, [1], 0.125)
+    assert status.item() == 0
+
+
+def test_nonfinite_keys_are_flagged_wherever_they_lie():
+    b = Batch(bt, [300], 16, 1, 64)
+    q = torch.from_numpy(b.queries(10, 3)).cuda()
+    for j in (0, 1, 15, 16, 63, 64, 127, 128, 200, 289):
+        page = b.table.pages[b.slots[0].item(), j // 16].item()
+        for value in (float("nan"), float("inf")):
+            was = b.cache.k[page, 0, j % 16, 7].item()
+            b.cache.k[page, 0, j % 16, 7] = value
+            for f in (lambda **kw: bt.bwta_attn_decode_paged(q[-1:], b.cache, b.table, 0.125, **kw),
+                      lambda **kw: bt.bwta_attn_prompt_paged(q, cu([0, 10]), b.cache, b.table, 0.125, **kw)):
+                status = bt.new_status()
+                f(slots=b.slots, status=status)
+                torch.cuda.synchronize()
+                assert status.item() == bt.STATUS_NONFINITE, (j, value)
+            b.cache.k[page, 0, j % 16, 7] = was
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_attention_with_bad_entries(e4m3):
     """Pages and slots outside, lengths past the row: flagged, nothing else disturbed."""
@@ -314,6 +353,124 @@ def test_nonfinite_inputs_are_flagged():
         f(window=40, slots=b.slots, status=status)            # key 3 is hidden now
         torch.cuda.synchronize()
         assert status.item() == 0
+
+
+def far_batch(lens, ps, H, D, e4m3, seed, gap):
+    """A batch whose pages lie `gap` elements apart: offsets pass 32 bits."""
+    b = Batch(bt, lens, ps, H, D, e4m3, seed=seed)
+    n = H * ps * D
+    ns = H * ps
+
+    def spread(t, step, inner):
+        buf = torch.empty(b.num_pages * step, dtype=t.dtype, device="cuda")
+        far = buf.as_strided(t.shape, (step, *inner))
+        far.copy_(t)
+        return far
+    k, v = (spread(t, gap, (ps * D, D, 1)) for t in (b.cache.k, b.cache.v))
+    sc = [None if t is None else spread(t, ns + 4, (ps, 1)) for t in (b.cache.k_scale, b.cache.v_scale)]
+    assert gap >= n and (b.num_pages - 1) * gap > 1 << 32
+    b.cache = bt.KvCache(k, v, *sc)
+    return b
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_offsets_past_32_bits(e4m3):
+    """Pages 2^28 elements apart (a pool of 2^32 and more): append, both attentions, copies."""
+    lens = [200, 90]
+    b = far_batch(lens, 16, 2, 64, e4m3, 3, 1 << 28)
+    q = b.queries(2, 4)
+    qt = torch.from_numpy(q).cuda()
+    out = bt.bwta_attn_decode_paged(qt, b.cache, b.table, 0.125, slots=b.slots)
+    b.check(q, out, [1, 1], 0.125)
+    out = bt.bwta_attn_prompt_paged(qt, cu([0, 1, 2]), b.cache, b.table, 0.125, slots=b.slots)
+    b.check(q, out, [1, 1], 0.125)
+    slot = b.slot_of[0]
+    last = b.table.pages[slot, (lens[0] - 1) // 16].item()
+    ones = torch.ones((1, 2, 64), device="cuda")
+    bt.bwta_kv_append(b.cache, b.table, ones, ones, slots=b.slots[:1])
+    assert (cache_values(type("C", (), dict(k=b.cache.k[last:last + 1], v=b.cache.v[last:last + 1],
+                                            k_scale=b.cache.k_scale[last:last + 1] if e4m3 else None,
+                                            v_scale=b.cache.v_scale[last:last + 1] if e4m3 else None)))[0]
+            [0, :, (lens[0] - 1) % 16] == 1).all()
+    free = b.num_pages - 1 if last != b.num_pages - 1 else b.num_pages - 2
+    bt.bwta_kv_copy_pages(b.cache, b.cache, cu([last]), cu([free]))
+    torch.cuda.synchronize()
+    assert torch.equal(b.cache.k[last].view(torch.uint8), b.cache.k[free].view(torch.uint8))
+    assert torch.equal(b.cache.v[last].view(torch.uint8), b.cache.v[free].view(torch.uint8))
+
+
+@pytest.mark.parametrize("H,G,D,ps,lens,news,window,sinks", [
+    (1, 2, 8, 16, [150, 33], [150, 20], 0, 0),
+    (2, 1, 24, 1024, [1500, 1024], [260, 129], 0, 0),
+    (1, 9, 104, 48, [400], [90], 70, 40),
+    (1, 2, 120, 65536, [700, 1], [300, 1], 0, 0),
+    (3, 2, 72, 112, [333, 112], [111, 112], 50, 3),
+    (1, 128, 64, 16, [40], [3], 0, 0),
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_odd_widths_pages_and_strides(H, G, D, ps, lens, news, window, sinks, e4m3):
+    """Head widths that are not multiples of 16, long pages, rows of q and out further apart than dense."""
+    b = Batch(bt, lens, ps, H, D, e4m3, seed=D)
+    heads, n = H * G, sum(news)
+    q = b.queries(n, heads)
+    for prompt in (True, False):
+        rows = n if prompt else len(lens)
+        buf = torch.full((2, rows, heads * D + 24), 3.25, dtype=torch.float16, device="cuda")
+        qt, out = (x[:, :heads * D].unflatten(1, (heads, D)) for x in buf)
+        qt.copy_(torch.from_numpy(q[:rows]))
+        status = bt.new_status()
+        args = dict(slots=b.slots, status=status, out=out)
+        if prompt:
+            bt.bwta_attn_prompt_paged(qt, offsets(news), b.cache, b.table, D ** -0.5, window, sinks, **args)
+        else:
+            bt.bwta_attn_decode_paged(qt, b.cache, b.table, D ** -0.5, window, sinks, **args)
+        torch.cuda.synchronize()
+        assert status.item() == 0 and (buf[:, :, heads * D:] == 3.25).all()
+        b.check(q, out, news if prompt else [1] * len(lens), D ** -0.5, window, sinks, rows=16)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_captured_prompt_follows_the_lengths(e4m3):
+    """One graph, replayed while the sequences grow: short, then long enough to be shared out."""
+    b = Batch(bt, [2500, 1800], 32, 2, 64, e4m3, seed=9)
+    q = b.queries(40, 6)
+    qt = torch.from_numpy(q).cuda()
+    off = cu([0, 30, 40])
+    full = b.table.kv_len.clone()
+    out = torch.empty_like(qt)
+    bt.bwta_attn_prompt_paged(qt, off, b.cache, b.table, 0.125, slots=b.slots, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bt.bwta_attn_prompt_paged(qt, off, b.cache, b.table, 0.125, slots=b.slots, out=out)
+    for cut in ((2500, 1800), (35, 10), (130, 700), (2500, 11)):
+        b.table.kv_len[b.slots.long()] = cu(list(cut))
+        graph.replay()
+        torch.cuda.synchronize()
+        sub = Batch.__new__(Batch)
+        sub.__dict__.update(b.__dict__)
+        sub.lens = list(cut)
+        sub.k, sub.v = ([x[:, :t] for x, t in zip(y, cut)] for y in (b.k, b.v))
+        sub.check(q, out, [30, 10], 0.125, rows=16)
+    b.table.kv_len.copy_(full)
+    graph.reset()
+
+
+def test_two_streams_at_once():
+    """Both attentions on two streams, many calls each, beside one another: no result depends on the other."""
+    b = Batch(bt, [3000, 500, 77], 16, 2, 128, True, seed=12)
+    q = torch.from_numpy(b.queries(60, 8)).cuda()
+    off = cu([0, 20, 40, 60])
+    want_d = bt.bwta_attn_decode_paged(q[:3], b.cache, b.table, 0.09, slots=b.slots)
+    want_p = bt.bwta_attn_prompt_paged(q, off, b.cache, b.table, 0.09, slots=b.slots)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((bt.bwta_attn_decode_paged(q[:3], b.cache, b.table, 0.09, slots=b.slots),
+                        bt.bwta_attn_prompt_paged(q, off, b.cache, b.table, 0.09, slots=b.slots)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(d, want_d) and torch.equal(p, want_p) for d, p in got)
 
 
 # ------------------------------------------------------------------ pages
