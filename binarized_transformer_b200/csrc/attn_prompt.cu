@@ -60,7 +60,7 @@ struct PrShape {
   static constexpr int NH = DP / 64;                  // halves of 64 columns
   static constexpr int TILE = NH * PR_T * 128;        // bytes of 128 rows
   static constexpr int SLOTS = DP == 128 ? (E4M3 ? 4 : 5) : 8;  // key and value tiles in the ring
-  static constexpr int RAW = E4M3 ? 16 * DP + 64 : 0;  // 16 rows as they lie in the cache, with their scales
+  static constexpr int RAW = E4M3 ? 16 * DP : 0;  // 16 rows as they lie in the cache
   static constexpr int BARS = 1024;
   static constexpr int SMEM = 1024 + (2 + SLOTS) * TILE + 16 * RAW + BARS;
   static_assert(SMEM <= 232448, "shared memory of a block");
@@ -119,12 +119,6 @@ __device__ __forceinline__ bool pr_wait(PrBars *b, uint64_t *bar, uint32_t parit
   return false;
 }
 
-__device__ __forceinline__ int pr_tile(const PrItem &it, int j) {
-  return j + (j < it.u_sink ? it.j0 : it.u_first);
-}
-__device__ __forceinline__ bool pr_active(const PrItem &it, int a, int t) {
-  return t <= it.last[a] && (t >= it.first[a] || t < it.sink[a]);
-}
 
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -372,13 +366,16 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       uint32_t halves = 0;  // of key tiles, so far
       const uint32_t ts = tmem_addr(tmem, q * 32, w * 128), to = tmem_addr(tmem, q * 32, 256 + w * 128);
       const uint64_t cc = pk2(c2, c2);
-      for (int j = 0; j < steps && ok; ++j) {
-        const int t = pr_tile(it, j);
-        if (!pr_active(it, w, t)) continue;
+      // in registers: every barrier would have them read again
+      const int n = steps, j0 = it.j0, u_sink = it.u_sink, u_first = it.u_first;
+      const int last = it.last[w], first = it.first[w], sink = it.sink[w];
+      for (int j = 0; j < n && ok; ++j) {
+        const int t = j + (j < u_sink ? j0 : u_first);  // the key tile
+        if (t > last || (t < first && t >= sink)) continue;
         for (int h = 0; h < 2; ++h, ++halves) {
-          const int j0 = t * PR_T + h * PR_HALF;
-          const bool all = j0 + PR_HALF - 1 <= p_min &&
-                           (!a.window || j0 > p_max - a.window || j0 + PR_HALF <= a.sinks);
+          const int k0 = t * PR_T + h * PR_HALF;
+          const bool all = k0 + PR_HALF - 1 <= p_min &&
+                           (!a.window || k0 > p_max - a.window || k0 + PR_HALF <= a.sinks);
           ok = __all_sync(FULL, pr_wait(bars, &bars->s_ready[w][h], (halves >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
@@ -387,9 +384,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
           tmem_ld32(ts + h * PR_HALF + 32, v[1]);
           tmem_wait_ld();
           if (!all) {
-            const int hi = valid ? p - j0 : -1;
-            const int lo = (int)min(max(lo64 - j0, (int64_t)0), (int64_t)PR_HALF);
-            const int sk = (int)min(max(a.sinks - j0, (int64_t)0), (int64_t)PR_HALF);
+            const int hi = valid ? p - k0 : -1;
+            const int lo = (int)min(max(lo64 - k0, (int64_t)0), (int64_t)PR_HALF);
+            const int sk = (int)min(max(a.sinks - k0, (int64_t)0), (int64_t)PR_HALF);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const uint32_t see = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
@@ -522,13 +519,18 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
     const uint32_t recip = 65536u / chunks + 1;  // p / chunks = (p * recip) >> 16 for p < 256
     bool bad = false;
     const uint32_t w2 = warp - 4;
+    // in registers: every barrier would have them read again
+    const int lo = it.lo, hi = it.hi, j0 = it.j0, u_sink = it.u_sink, u_first = it.u_first;
+    const int64_t head_row = (int64_t)it.head * a.c.ps;
     // 16 tokens of key tile j (and their values): the offset of the first (in
     // elements; scales: in floats), which of the 16 rows to read
     struct Place {
       int64_t at, sat;
       uint32_t rows;
     };
-    auto token = [&](int j, int gi) { return pr_tile(it, j) * PR_T + (int)(w2 * GROUPS + gi) * 16; };
+    auto token = [&](int j, int gi) {
+      return (j + (j < u_sink ? j0 : u_first)) * PR_T + (int)(w2 * GROUPS + gi) * 16;
+    };
     // tok / ps, both multiples of 16: the quotient of a multiplication is right or 1 short
     const uint32_t ps16 = a.c.ps / 16, by_ps = 0xffffffffu / ps16;
     const int32_t *row_of_pages = a.r.pages + (int64_t)it.slot * a.r.ld;
@@ -545,17 +547,17 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
     auto page_of = [&](int j, int gi) -> int32_t {
       const int tok = token(j, gi);
       int in;
-      return j < steps && tok <= it.hi ? row_of_pages[split(tok, in)] : -1;
+      return j < steps && tok <= hi ? row_of_pages[split(tok, in)] : -1;
     };
     auto place = [&](int j, int gi, int32_t page) -> Place {
       const int tok = token(j, gi);
       Place p{0, 0, 0};
       // bit r: token tok + r is seen by some row
-      const int top = min(it.hi - tok + 1, 16);
+      const int top = min(hi - tok + 1, 16);
       if (top <= 0) return p;
       p.rows = (1u << top) - 1;
-      if (a.window && tok < it.lo) {
-        const uint32_t win = it.lo - tok >= 16 ? 0u : 0xffffu << (it.lo - tok);
+      if (a.window && tok < lo) {
+        const uint32_t win = lo - tok >= 16 ? 0u : 0xffffu << (lo - tok);
         const int64_t sk = a.sinks - tok;
         p.rows &= win | (sk >= 16 ? 0xffffu : sk <= 0 ? 0u : (1u << sk) - 1);
         if (!p.rows) return p;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       }
       int in;
       split(tok, in);
-      const int64_t row = (int64_t)it.head * a.c.ps + in;
+      const int64_t row = head_row + in;
       p.at = (int64_t)page * a.c.page_stride + row * D;
       p.sat = (int64_t)page * a.c.scale_stride + row;
       return p;
@@ -629,6 +631,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       int32_t page = page_of(0, 0);
       Place pl;          // of the tile whose copies are under way
       uint32_t rows[2];  // visible ones of the pieces in the ring
+      float sc[2] = {0, 0};  // and the scales of their rows (lanes 16 .. 31: again)
       uint32_t fetched[2] = {0, 0};
       auto fetch = [&](int q) {  // piece q: keys (0) or values (1)
         const Place &p = pl;
@@ -637,9 +640,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         uint64_t *bar = &bars->raw[w2][q];
         if (p.rows) {
           const uint32_t on = lane == 0;
-          mbar_arrive_expect_tx_if(on, bar, 16 * D + 64);
+          mbar_arrive_expect_tx_if(on, bar, 16 * D);
           bulk_load_if(on, raw + q * S::RAW, (q == 0 ? a.c.k : a.c.v) + p.at, 16 * D, bar);
-          bulk_load_if(on, raw + q * S::RAW + 16 * DP, (q == 0 ? a.c.ks : a.c.vs) + p.sat, 64, bar);
+          sc[q] = (q == 0 ? a.c.ks : a.c.vs)[p.sat + (lane & 15)];
         } else if (lane == 0) {
           mbar_arrive(bar);
         }
@@ -666,8 +669,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
           if (!ok) break;
           uint8_t *st = slot_of(u);
           const uint8_t *from = raw + q * S::RAW;
-          const float sc = *reinterpret_cast<const float *>(from + 16 * DP + (lane & 15) * 4);
-          uint32_t one = (uint32_t)__half_as_ushort(__float2half_rn(sc));
+          uint32_t one = (uint32_t)__half_as_ushort(__float2half_rn(sc[q]));
           one |= one << 16;
           if (D == DP && rows[q] == 0xffffu) {
             // all loads, then all stores: nothing waits for a piece by itself
