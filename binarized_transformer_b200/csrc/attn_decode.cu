@@ -185,6 +185,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   return h;
 }
+// Four E4M3 bytes as two pairs of halves.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
 __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -433,8 +440,9 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
             ldsm4(st + ring_at<S::ROW>(h * 16 + (mat & 1) * 8 + mr, ks + mat / 2), r);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              const uint32_t ka[4] = {e4m3x2_to_half2(r[2 * p]), e4m3x2_to_half2(r[2 * p + 1]),
-                                      e4m3x2_to_half2(r[2 * p] >> 16), e4m3x2_to_half2(r[2 * p + 1] >> 16)};
+              uint32_t ka[4];
+              e4m3x4_to_half2(r[2 * p], ka[0], ka[2]);
+              e4m3x4_to_half2(r[2 * p + 1], ka[1], ka[3]);
 #pragma unroll
               for (int b = 0; b < NB; ++b) mma16816(s[h][b], ka, qb[b][ks + p][0], qb[b][ks + p][1]);
             }
@@ -543,10 +551,14 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const uint32_t x = r[2 * p], y = r[2 * p + 1];
-              const uint32_t vv[4] = {mul_half2(e4m3x2_to_half2(__byte_perm(x, 0, 0x20)), v01),
-                                      mul_half2(e4m3x2_to_half2(__byte_perm(x, 0, 0x31)), v01),
-                                      mul_half2(e4m3x2_to_half2(__byte_perm(y, 0, 0x20)), v23),
-                                      mul_half2(e4m3x2_to_half2(__byte_perm(y, 0, 0x31)), v23)};
+              // bytes 0, 2 (the even column of two tokens) and 1, 3 (the odd one)
+              uint32_t vv[4];
+              e4m3x4_to_half2(__byte_perm(x, 0, 0x3120), vv[0], vv[1]);
+              e4m3x4_to_half2(__byte_perm(y, 0, 0x3120), vv[2], vv[3]);
+              vv[0] = mul_half2(vv[0], v01);
+              vv[1] = mul_half2(vv[1], v01);
+              vv[2] = mul_half2(vv[2], v23);
+              vv[3] = mul_half2(vv[3], v23);
 #pragma unroll
               for (int b = 0; b < NB; ++b) mma16816(o[b][ks + p], vv, pb[h][b][0], pb[h][b][1]);
             }
