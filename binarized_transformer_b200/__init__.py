@@ -474,7 +474,7 @@ class KvCache:
     (E4M3 bytes) with fp32 scales [num_pages, n_kv_heads, page_size]. Pages may be further apart than
     dense (a view of a larger buffer), the inner dimensions are dense. Keeps the tensors alive; their
     storage must stay where it is."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "ref", "device")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "ref", "device", "n_kv_heads", "head_dim")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         e4m3 = k.dtype == torch.uint8
@@ -500,7 +500,7 @@ class KvCache:
             ls = stride(k_scale, rows)
             assert stride(v_scale, rows) == ls
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self.n_kv_heads, self.head_dim = k.device, H, D
         self.c = KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                           v_scale.data_ptr() if e4m3 else None, P, ps, H, D, ld, ls,
                           KV_E4M3 if e4m3 else KV_F16)
@@ -626,7 +626,7 @@ def bwta_kv_append(cache: KvCache, table: KvTable, k, v, slots=None, cu_q=None, 
     cu_q[s] .. cu_q[s+1] belong to sequence s and end at its kv_len."""
     dev = cache.device
     assert table.device == dev and k.dtype == v.dtype and k.dtype in (torch.float16, torch.float32)
-    width = cache.c.n_kv_heads * cache.c.head_dim
+    width = cache.n_kv_heads * cache.head_dim
     kp, ldk, n = _kv_rows(k, width, dev)
     vp, ldv, nv = _kv_rows(v, width, dev)
     assert n == nv
@@ -647,15 +647,17 @@ def bwta_attn_decode_paged(q, cache: KvCache, table: KvTable, softmax_scale: flo
                            sinks: int = 0, slots=None, workspace=None, status=None, out=None):
     """Attention of one new token of each sequence over its pages. q fp16 [n_seq, n_heads, head_dim]
     -> out, the same shape. workspace: uint8 of decode_workspace() bytes (allocated when not given)."""
-    dev, D = cache.device, cache.c.head_dim
+    dev, D = cache.device, cache.head_dim
     assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
     n, heads = q.shape[0], q.shape[1]
     qp, ldq, _ = _kv_rows(q, heads * D, dev)
     n_seq = _n_seq(table, slots, None, n)
     if out is None:
         out = torch.empty((n, heads, D), dtype=torch.float16, device=dev)
-    assert out.dtype == torch.float16 and out.shape == q.shape
-    op, ldo, _ = _kv_rows(out, heads * D, dev)
+        op, ldo = out.data_ptr(), heads * D
+    else:
+        assert out.dtype == torch.float16 and out.shape == q.shape
+        op, ldo, _ = _kv_rows(out, heads * D, dev)
     if workspace is None:
         workspace = decode_workspace(heads, cache)
     assert workspace.device == dev and workspace.is_contiguous()
@@ -668,8 +670,7 @@ def bwta_attn_decode_paged(q, cache: KvCache, table: KvTable, softmax_scale: flo
 
 def decode_workspace(n_heads: int, cache: KvCache):
     """A workspace for bwta_attn_decode_paged; calls that may overlap in time need one each."""
-    c = cache.c
-    n = _workspace_bytes("bwta_attn_decode_workspace", n_heads, c.n_kv_heads, c.head_dim)
+    n = _workspace_bytes("bwta_attn_decode_workspace", n_heads, cache.n_kv_heads, cache.head_dim)
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
@@ -678,15 +679,17 @@ def bwta_attn_prompt_paged(q, cu_q, cache: KvCache, table: KvTable, softmax_scal
     """Attention of many new tokens of each sequence over its pages, which hold them already.
     q fp16 [rows, n_heads, head_dim], rows cu_q[s] .. cu_q[s+1] the newest of sequence s -> out, the
     same shape (rows past the last sequence are left as they are)."""
-    dev, D = cache.device, cache.c.head_dim
+    dev, D = cache.device, cache.head_dim
     assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
     n, heads = q.shape[0], q.shape[1]
     qp, ldq, _ = _kv_rows(q, heads * D, dev)
     n_seq = _n_seq(table, slots, cu_q, n)
     if out is None:
         out = torch.empty((n, heads, D), dtype=torch.float16, device=dev)
-    assert out.dtype == torch.float16 and out.shape == q.shape
-    op, ldo, _ = _kv_rows(out, heads * D, dev)
+        op, ldo = out.data_ptr(), heads * D
+    else:
+        assert out.dtype == torch.float16 and out.shape == q.shape
+        op, ldo, _ = _kv_rows(out, heads * D, dev)
     _kv_call("bwta_attn_prompt_paged", dev, cache.ref, table.ref, _ints(slots, dev), n_seq,
              _ints(cu_q, dev), n, qp, ldq, heads, softmax_scale, window,
              sinks, op, ldo, _status(status, dev))

@@ -128,6 +128,12 @@ __device__ __forceinline__ int dec_scan(const AttnArgs &a, int64_t *before, int6
   return per;
 }
 
+// a / b for a >= 0, b > 0; a division in 64 bits takes several times as long.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // How the units are cut: block c has [start(c), start(c + 1)).
 struct DecCut {
   int64_t total;
@@ -135,8 +141,8 @@ struct DecCut {
   __device__ DecCut(int64_t t, int most) : total(t) {
     blocks = (int)min((int64_t)most, (t + DEC_MIN_UNITS - 1) / DEC_MIN_UNITS);
   }
-  __device__ int64_t start(int c) const { return total * c / blocks; }
-  __device__ int owner(int64_t u) const { return (int)(((u + 1) * blocks - 1) / total); }
+  __device__ int64_t start(int c) const { return div_pos(total * c, blocks); }
+  __device__ int owner(int64_t u) const { return (int)div_pos((u + 1) * blocks - 1, total); }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool read) {
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
       u -= (int64_t)at.q.units * items;
       at.q = dec_seq<TILE>(a, ++at.s);
     }
-    at.item = (int)(u / at.q.units);
+    at.item = (int)div_pos(u, at.q.units);
     at.unit = (int)(u - (int64_t)at.item * at.q.units);
   }
   __syncthreads();  // the prefix sums have been read: `joint` may be written
@@ -683,7 +689,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
   int64_t u = 0;
   int first = 0, last = 0, row = 0;
   if (h < a.n_heads && q.units > 0) {
-    const int who = (int)(s / per), kh = h / heads, hg = (h - kh * heads) / A.per_item;
+    const int who = (int)div_pos(s, per), kh = h / heads, hg = (h - kh * heads) / A.per_item;
     u = before[who] * items;
     for (int64_t i = (int64_t)who * per; i < s; ++i) u += (int64_t)dec_seq<TILE>(a, i).units * items;
     u += (int64_t)(kh * A.groups + hg) * q.units;
@@ -702,9 +708,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
     return;
   }
   if (first == last) return;  // written by that block
-  // a piece is its block's second one when the item begins in that block
+  // a piece is its block's second one where the item begins: in the first block
   auto piece = [&](int c) {
-    return A.ws + ((size_t)(c * 2 + (cut.start(c) <= u ? 1 : 0)) * A.rows + row) * (DP + 2);
+    return A.ws + ((size_t)(c * 2 + (c == first ? 1 : 0)) * A.rows + row) * (DP + 2);
   };
   constexpr int BY = WIDE ? JOIN_HEADS : 1;
   float M = -INFINITY, L = 0.0f, y[4] = {0, 0, 0, 0};

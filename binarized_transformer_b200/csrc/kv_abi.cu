@@ -93,6 +93,8 @@ int attn_args(const bwta_kv_cache *cache, const bwta_kv_table *table, const int3
   if (int r = check_seqs(table, slots, n_seq, cu_q, total_q)) return r;
   if (n_heads < 1 || n_heads % cache->n_kv_heads != 0) return BWTA_ERR_INVALID_ARG;
   if (n_heads > 65535) return BWTA_ERR_UNSUPPORTED;
+  // positions and tiles are counted in 32 bits
+  if (table->max_pages * cache->page_size > I32_MAX - 65536) return BWTA_ERR_UNSUPPORTED;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return BWTA_ERR_INVALID_ARG;
   if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return BWTA_ERR_INVALID_ARG;
   const int64_t width = n_heads * cache->head_dim;

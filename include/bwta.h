@@ -441,7 +441,8 @@ int bwta_kv_append(const bwta_kv_cache *cache, const bwta_kv_table *table, const
  *           preparation and do not outlive the call. Calls that can run at the
  *           same time need one each.
  *  softmax_scale finite and > 0; n_heads a multiple of n_kv_heads; q and out
- *  16-byte aligned, strides multiples of 8 elements.
+ *  16-byte aligned, strides multiples of 8 elements; max_pages * page_size at most
+ *  2^31 - 2^16 - 1 (UNSUPPORTED above).
  *  BAD_PAGE: a page outside the pool, a slot outside the table (read as empty)
  *  or a length past the row of pages (cut there); the outputs of that sequence
  *  are unspecified. NONFINITE: an output is not finite, because a visible key

@@ -124,6 +124,7 @@ def test_attention_arguments(lib, f):
     assert f(lib, ldq=255) == I and f(lib, ldo=248) == I and f(lib, q=None) == I and f(lib, out=None) == I
     assert f(lib, q=Q) == A and f(lib, out=Q) == A and f(lib, ldq=260) == A and f(lib, ldo=260) == A
     assert f(lib, heads=65536, ldq=1 << 23, ldo=1 << 23) == U
+    assert f(lib, t=table(mp=1 << 27, ld=1 << 27)) == U     # positions past 31 bits
     assert f(lib, n_seq=0, **(dict(total=0) if f is prompt else {})) == bt.BWTA_OK
 
 
