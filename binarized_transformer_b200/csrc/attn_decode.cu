@@ -33,6 +33,14 @@
 // to fp16 for the second product, l sums it unrounded. E4M3: K's scale is applied
 // to the scores in fp32; V's, a power of two, to the converted values, which stays
 // exact.
+//
+// Measured on a B200 (a copy moves 6.55 TB/s): fp16, 64 sequences of 0 .. 8191 tokens,
+// 64 query heads on 8 key heads of 128: 1.29 GB in 210 us, 0.94 of the copy's rate;
+// E4M3, 32 sequences, window 4096, 32 heads: 1.10 GB in 200 us, 0.83, bound by the
+// issue of the conversions at 12 warps an SM (45% of the slots; four blocks of 16-token
+// steps 232 us, two of 32-token ones 244); E4M3, one sequence of 250,001 tokens: 0.53 GB
+// in 98 us, 0.82. One token over 333 in fp16: 12.8 us, launches and the two chains of
+// dependent loads (length, page, keys; length, pieces).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -42,7 +50,6 @@ namespace bwta {
 
 constexpr int DEC_WARPS = 4, DEC_THREADS = DEC_WARPS * 32;
 constexpr int DEC_MAX_ROWS = 16;  // query heads of an item at most
-constexpr int DEC_MIN_UNITS = 1;  // units that a block takes at least
 constexpr int DEC_MAX_BLOCKS = 640;
 constexpr float DEC_SLACK = 8.0f;  // how far scores may pass the reference (log2)
 constexpr int JOIN_THREADS = 256, JOIN_HEADS = JOIN_THREADS / 32;
@@ -54,7 +61,7 @@ struct DecShape {
   static constexpr int SUB = dec_tile(E4M3) / DEC_WARPS;  // tokens of one warp in a unit
   static constexpr int TILE = dec_tile(E4M3);
   static constexpr int ROW = DP * (E4M3 ? 1 : 2);      // bytes of a token's row in the ring
-  static constexpr int BLOCKS = NB == 1 ? 3 : 2;  // on an SM
+  static constexpr int BLOCKS = NB == 1 ? 3 : 2;  // on an SM; two for up to 8 heads: E4M3 244 us for 211
   static constexpr int STAGES = (NB == 1 ? 2 : 3) * (DP == 64 ? 2 : 1);
   static constexpr int HALF = SUB * ROW;               // keys (or values) of a stage
   static constexpr int STAGE = 2 * HALF + (E4M3 ? 2 * SUB * 4 : 0);
@@ -139,7 +146,7 @@ struct DecCut {
   int64_t total;
   int blocks;
   __device__ DecCut(int64_t t, int most) : total(t) {
-    blocks = (int)min((int64_t)most, (t + DEC_MIN_UNITS - 1) / DEC_MIN_UNITS);
+    blocks = (int)min((int64_t)most, t);
   }
   __device__ int64_t start(int c) const { return div_pos(total * c, blocks); }
   __device__ int owner(int64_t u) const { return (int)div_pos((u + 1) * blocks - 1, total); }

@@ -6,7 +6,9 @@
 // each) holds one row of k and the same row of v, both loaded before either is
 // used; the maximum is taken over the group in registers. One pass: bound by
 // HBM (8 or 4 bytes read and 1 or 2 written an element), at the sizes of one
-// decode step by the latency of kv_len -> page -> store.
+// decode step by the latency of kv_len -> page -> store. Measured (B200): 7 prompts,
+// 10,600 tokens of 32 heads of 128, fp32 into fp16, 523 MB in 88 us (5.95 TB/s, 0.91 of
+// a copy; with one head a group 128 us); 64 tokens of 8 heads into E4M3 4.7 us.
 #include <algorithm>
 
 #include "kv.cuh"
