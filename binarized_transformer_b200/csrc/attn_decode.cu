@@ -16,6 +16,10 @@
 // on after it) and k_attn_join adds them in the order of the blocks, so the order
 // of every sum is fixed by the lengths alone.
 //
+// Few items of no great length (CLUSTER) are the latency case: a cluster of 2 .. 8
+// blocks takes an item, each an equal share of its tiles, and adds the parts up over
+// distributed shared memory. No prefix sums, no second launch.
+//
 // Inside a block each of the 4 warps takes 16 (32) tokens of a tile. page_size is a
 // multiple of 16, so 16 tokens lie in one page and are one contiguous piece of it.
 // A warp copies its tokens into a ring of its own (cp.async, rows that are
@@ -39,8 +43,8 @@
 // E4M3, 32 sequences, window 4096, 32 heads: 1.10 GB in 200 us, 0.83, bound by the
 // issue of the conversions at 12 warps an SM (45% of the slots; four blocks of 16-token
 // steps 232 us, two of 32-token ones 244); E4M3, one sequence of 250,001 tokens: 0.53 GB
-// in 98 us, 0.82. One token over 333 in fp16: 12.8 us, launches and the two chains of
-// dependent loads (length, page, keys; length, pieces).
+// in 98 us, 0.82. One token over 333 in fp16, in clusters: 10.7 us, the launch and the
+// chain length, page, keys, parts.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -79,6 +83,7 @@ struct DecArgs {
   int per_item;  // query heads of one: 8 or 16
   int rows;    // heads of an item at most (rows of a piece in the workspace)
   int blocks;  // of k_attn_decode
+  int cluster; // blocks of an item (CLUSTER)
 };
 
 // A sequence's tiles with a visible key: [0, sink_tiles) and [first, tiles).
@@ -133,12 +138,6 @@ __device__ __forceinline__ int dec_scan(const AttnArgs &a, int64_t *before, int6
   if (threadIdx.x == 0) before[T] = total;
   __syncthreads();
   return per;
-}
-
-// a / b for a >= 0, b > 0; a division in 64 bits takes several times as long.
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-  if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
 }
 
 // How the units are cut: block c has [start(c), start(c + 1)).
@@ -240,7 +239,7 @@ struct DecCursor {
   __device__ int tile() const { return unit < q.sink_tiles ? unit : q.first + unit - q.sink_tiles; }
 };
 
-template <int DP, bool E4M3, int NB>
+template <int DP, bool E4M3, int NB, bool CLUSTER>
 __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k_attn_decode(const DecArgs A) {
   using S = DecShape<DP, E4M3, NB>;
   constexpr int SUB = S::SUB, TILE = S::TILE, MT = SUB / 16, KS = DP / 16, ROWS = 8 * NB;
@@ -257,16 +256,24 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
       *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0, 0, 0, 0);
   pdl_wait();
   pdl_trigger();  // after the wait: k_attn_join may then read the lengths before its own
-  const int per = dec_scan<DEC_THREADS, TILE>(a, before, sums);  // its barriers cover the zeros
-  const DecCut cut(before[DEC_THREADS] * items, A.blocks);
-  if ((int)blockIdx.x >= cut.blocks) return;
-  const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
-  const int n = (int)(u1 - u0);
-  if (n == 0) return;
-
-  // the sequence, item and tile of unit u0
   DecCursor<TILE> at;
-  {
+  int n = 0;
+  if (CLUSTER) {
+    const int id = blockIdx.x / A.cluster, rank = blockIdx.x - id * A.cluster;
+    const int s = id / items;
+    at.s = s;
+    at.item = id - s * items;
+    at.q = dec_seq<TILE>(a, s);
+    at.unit = (int)div_pos((int64_t)at.q.units * rank, A.cluster);
+    n = (int)div_pos((int64_t)at.q.units * (rank + 1), A.cluster) - at.unit;
+  } else {
+    const int per = dec_scan<DEC_THREADS, TILE>(a, before, sums);
+    const DecCut cut(before[DEC_THREADS] * items, A.blocks);
+    if ((int)blockIdx.x >= cut.blocks) return;
+    const int64_t u0 = cut.start(blockIdx.x);
+    n = (int)(cut.start(blockIdx.x + 1) - u0);
+    if (n == 0) return;
+    // the sequence, item and tile of unit u0
     int lo = 0, hi = DEC_THREADS - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
     at.item = (int)div_pos(u, at.q.units);
     at.unit = (int)(u - (int64_t)at.item * at.q.units);
   }
-  __syncthreads();  // the prefix sums have been read: `joint` may be written
+  __syncthreads();  // the zeros are there, the prefix sums have been read: `joint` may be written
   bool bad = false, finite = true;
 
   // ---- the copies run ahead: their own position, with the entry of the row of pages
@@ -630,7 +637,22 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
         if (warp == 0) take(joint);
         __syncthreads();
       }
-      if (warp == 0) {
+      if (CLUSTER && warp == 0) {
+        // this block's share, rows of DP sums, the maximum and the sum of weights
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float *row = joint + (8 * b + 2 * t + e) * (DP + 2);
+            if (g == 0) *reinterpret_cast<float2 *>(row + DP) = make_float2(m[b][e], l[b][e]);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const int c0 = ks * 16 + (E4M3 ? 2 * g : g), c1 = c0 + (E4M3 ? 1 : 8);
+              row[c0] = o[b][ks][e];
+              row[c1] = o[b][ks][2 + e];
+            }
+          }
+      } else if (warp == 0) {
         const bool began = i >= at.unit;  // the item's first unit is this block's too
         const bool whole = began && item_ends;
 #pragma unroll
@@ -672,6 +694,46 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
     if (i + 1 < n) step(at);
   }
   cp_wait<0>();
+  if (CLUSTER) {
+    if (n == 0 && threadIdx.x < ROWS)
+      *reinterpret_cast<float2 *>(joint + threadIdx.x * (DP + 2) + DP) = make_float2(-INFINITY, 0.0f);
+    __syncwarp();
+    cluster_sync();
+    // each block adds up some rows: a warp a row, 4 columns a lane
+    const int rank = blockIdx.x % A.cluster, kh = at.item / A.groups, h0 = (at.item - kh * A.groups) * ROWS;
+    const uint32_t part = smem_addr(joint);
+    if (rank == 0 && threadIdx.x == 0) bad |= at.q.bad;
+    for (int row = rank + warp * A.cluster; row < min(ROWS, heads - h0); row += DEC_WARPS * A.cluster) {
+      float M = -INFINITY, L = 0.0f, y[4] = {0, 0, 0, 0};
+      for (int k = 0; k < A.cluster; ++k) M = fmaxf(M, cluster_ld2(part + (row * (DP + 2) + DP) * 4, k).x);
+      for (int k = 0; k < A.cluster; ++k) {
+        const float2 ml = cluster_ld2(part + (row * (DP + 2) + DP) * 4, k);
+        if (ml.x == -INFINITY) continue;  // no visible key there
+        const float f = exp2_fast(ml.x - M);
+        L += ml.y * f;
+        if (lane * 4 < D) {
+          const float2 v0 = cluster_ld2(part + (row * (DP + 2) + lane * 4) * 4, k);
+          const float2 v1 = cluster_ld2(part + (row * (DP + 2) + lane * 4 + 2) * 4, k);
+          y[0] += v0.x * f;
+          y[1] += v0.y * f;
+          y[2] += v1.x * f;
+          y[3] += v1.y * f;
+        }
+      }
+      if (lane * 4 < D) {
+        const float inv = at.q.units ? 1.0f / L : 0.0f;  // an empty sequence: zeros
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] *= inv;
+          finite &= y[e] - y[e] == 0.0f;
+        }
+        *reinterpret_cast<uint2 *>(a.out + at.s * a.ldo + (int64_t)(kh * heads + h0 + row) * D + lane * 4) =
+            make_uint2(half2_bits(y[0], y[1]), half2_bits(y[2], y[3]));
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its part is read
+  }
   if (bad) flag_status(a.d_status, BWTA_STATUS_BAD_PAGE);
   if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);
 }
@@ -796,19 +858,35 @@ int64_t attn_decode_ws(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
 
 template <int DP, bool E4M3, int NB>
 static cudaError_t launch_decode_t(DecArgs A, cudaStream_t s) {
-  static SmemOptIn opt_in;
-  auto kern = k_attn_decode<DP, E4M3, NB>;
-  constexpr int smem = DecShape<DP, E4M3, NB>::SMEM;
-  if (cudaError_t e = opt_in(kern, smem, true)) return e;
+  using S = DecShape<DP, E4M3, NB>;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  A.blocks = std::min(std::max(sms, 1) * DecShape<DP, E4M3, NB>::BLOCKS, DEC_MAX_BLOCKS);
-  if (cudaError_t e = launch_pdl(kern, dim3(A.blocks), dim3(DEC_THREADS), smem, s, A)) return e;
+  A.blocks = std::min(std::max(sms, 1) * S::BLOCKS, DEC_MAX_BLOCKS);
+  // Clusters where all items run at once and no block can get more than 8 tiles (measured: one
+  // token over 333 12.8 -> 10.7 us; the other way spreads any length over the whole GPU).
+  const AttnArgs &a = A.a;
+  const int64_t items = a.n_seq * a.c.H * A.groups;
+  int64_t tiles = ceil_div<int64_t>((int64_t)a.r.max_pages * a.c.ps, S::TILE);
+  if (a.window)
+    tiles = std::min(tiles, a.window / S::TILE + 2 + std::min(tiles, ceil_div<int64_t>(a.sinks, S::TILE)));
+  for (A.cluster = 8; A.cluster >= 2; A.cluster /= 2) {
+    if (items * A.cluster > A.blocks) continue;
+    if (tiles > 8 * A.cluster) break;
+    static SmemOptIn opt_in;
+    auto kern = k_attn_decode<DP, E4M3, NB, true>;
+    if (cudaError_t e = opt_in(kern, S::SMEM, true)) return e;
+    return launch_pdl_cluster(kern, dim3((unsigned)(items * A.cluster)), (unsigned)A.cluster, dim3(DEC_THREADS),
+                              S::SMEM, s, A);
+  }
+  static SmemOptIn opt_in;
+  auto kern = k_attn_decode<DP, E4M3, NB, false>;
+  if (cudaError_t e = opt_in(kern, S::SMEM, true)) return e;
+  if (cudaError_t e = launch_pdl(kern, dim3(A.blocks), dim3(DEC_THREADS), S::SMEM, s, A)) return e;
   // An item of a call with few of them is cut into many pieces.
-  const bool wide = A.a.n_seq * A.a.c.H * A.groups * 16 <= A.blocks;
-  const int64_t joins = A.a.n_seq * (wide ? A.a.n_heads : ceil_div<int64_t>(A.a.n_heads, JOIN_HEADS));
-  return launch_pdl(wide ? k_attn_join<DP, dec_tile(E4M3), true> : k_attn_join<DP, dec_tile(E4M3), false>,
+  const bool wide = items * 16 <= A.blocks;
+  const int64_t joins = a.n_seq * (wide ? a.n_heads : ceil_div<int64_t>(a.n_heads, JOIN_HEADS));
+  return launch_pdl(wide ? k_attn_join<DP, S::TILE, true> : k_attn_join<DP, S::TILE, false>,
                     dim3((unsigned)joins), dim3(JOIN_THREADS), 0, s, A);
 }
 

@@ -159,7 +159,7 @@ __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
       c0 = min(max((int64_t)a.cu_q[s], (int64_t)0), a.total_q);
       c1 = min(max((int64_t)a.cu_q[s + 1], c0), a.total_q);
     }
-    const int64_t pairs = (c1 - c0 + two - 1) / two;
+    const int64_t pairs = div_pos(c1 - c0 + two - 1, two);
     int64_t x = pairs * H;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -173,7 +173,7 @@ __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
     }
     if (lane == __ffs(hit) - 1) {
       const int64_t local = at - (before + x - pairs * H);
-      const int64_t head = local / pairs, pair = pairs - 1 - (local - head * pairs);
+      const int64_t head = div_pos(local, pairs), pair = pairs - 1 - (local - head * pairs);
       const int64_t n = c1 - c0;
       bool bad = false;
       it.slot = kv_slot(a.r, s);
@@ -219,31 +219,6 @@ __device__ __forceinline__ void pr_find(const PrArgs &A, PrItem &it) {
     }
     return;
   }
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// What lies at shared-memory address `at` of block `rank` of the cluster.
-__device__ __forceinline__ float2 cluster_ld2(uint32_t at, int rank) {
-  float2 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
-      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y)
-      : "r"(at), "r"(rank)
-      : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 cluster_ld4(uint32_t at, int rank) {
-  float4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(at), "r"(rank)
-      : "memory");
-  return v;
 }
 
 // Eight E4M3 bytes as halves times their row's scale (both exact in fp16).
@@ -486,7 +461,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         *reinterpret_cast<float2 *>(base + (w * PR_T + r) * 8) = make_float2(m, l);
       } else if (ok && blockIdx.x % A.split == 0) {
         tc_fence_after();
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a row that sees nothing: zeros
+        const bool none = !(l > 0.0f || l != l);  // a row that sees nothing: zeros
+        const float inv = 1.0f / l;
+        float zero = 0.0f;  // stays 0 unless an output is not finite
         // through shared memory (Q has been read), so that rows are written whole
 #pragma unroll 1
         for (int c = 0; c * 32 < D; ++c) {
@@ -500,9 +477,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = inv == 0.0f ? 0.0f : __uint_as_float(o[i * 8 + 2 * e]) * inv;
-              const float y = inv == 0.0f ? 0.0f : __uint_as_float(o[i * 8 + 2 * e + 1]) * inv;
-              if (valid && c * 32 + i * 8 < D) finite &= x - x == 0.0f && y - y == 0.0f;
+              const float x = none ? 0.0f : __uint_as_float(o[i * 8 + 2 * e]) * inv;
+              const float y = none ? 0.0f : __uint_as_float(o[i * 8 + 2 * e + 1]) * inv;
+              if (c * 32 + i * 8 < D) zero = fmaf(x, 0.0f, fmaf(y, 0.0f, zero));
               const __half2 two = __floats2half2_rn(x, y);
               h[e] = *reinterpret_cast<const uint32_t *>(&two);
             }
@@ -511,15 +488,16 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
                 make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
+        finite = !valid || zero == 0.0f;
         __syncwarp();
         uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R) * a.ldo + (int64_t)it.head * A.group * D;
-#pragma unroll 1
+#pragma unroll 4
         for (int p = lane; p < 32 * chunks; p += 32) {
           const int r0 = (int)((p * by_chunks) >> 16), c = p - r0 * chunks, rr = q * 32 + r0;
-          if (rr >= used) break;
           const int i = (int)((rr * by_group) >> 16);
-          *reinterpret_cast<uint4 *>(out + (int64_t)i * a.ldo + (int64_t)(rr - i * A.group) * D + c * 8) =
-              *reinterpret_cast<const uint4 *>(qs + (c / 8) * (PR_T * 128) + swz128(rr, c % 8));
+          const uint4 y = *reinterpret_cast<const uint4 *>(qs + (c / 8) * (PR_T * 128) + swz128(rr, c % 8));
+          if (rr < used)
+            *reinterpret_cast<uint4 *>(out + (int64_t)i * a.ldo + (int64_t)(rr - i * A.group) * D + c * 8) = y;
         }
       }
       if (!finite) flag_status(a.d_status, BWTA_STATUS_NONFINITE);

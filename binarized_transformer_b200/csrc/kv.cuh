@@ -59,6 +59,38 @@ __device__ __forceinline__ int64_t kv_find_seq(const int32_t *cu, int64_t n, int
   return lo;
 }
 
+// a / b for a >= 0, b > 0; a division in 64 bits takes several times as long.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+// ---- blocks of a cluster
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What lies at shared-memory address `at` of block `rank` of the cluster.
+__device__ __forceinline__ float2 cluster_ld2(uint32_t at, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
 struct AttnArgs {
   KvView c;
   KvRows r;

@@ -163,6 +163,45 @@ def test_decode(H, G, D, ps, lens, window, sinks, e4m3):
     b.check(q, out, [1 if n else 0 for n in lens] if 0 not in lens else [1] * len(lens), D ** -0.5, window, sinks)
 
 
+@pytest.mark.parametrize("H,G,D,ps,lens,window,sinks", DECODE)
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_in_long_rows(H, G, D, ps, lens, window, sinks, e4m3):
+    """The same sequences in a table with room for long ones: the lengths are not bounded by its rows,
+    and the tiles of all sequences are shared out over the GPU."""
+    b = Batch(bt, lens, ps, H, D, e4m3, seed=len(lens) + D)
+    rows = torch.full((b.table.pages.shape[0], (1 << 20) // ps), -1, dtype=torch.int32, device="cuda")
+    rows[:, :b.max_pages] = b.table.pages
+    table = bt.KvTable(rows, b.table.kv_len)
+    q = b.queries(len(lens), H * G)
+    qt = torch.from_numpy(q).cuda()
+    status = bt.new_status()
+    out = bt.bwta_attn_decode_paged(qt, b.cache, table, D ** -0.5, window, sinks, slots=b.slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    b.check(q, out, [1] * len(lens), D ** -0.5, window, sinks)
+
+
+@pytest.mark.parametrize("n,H,G,ps,most", [(1, 1, 1, 16, 333), (1, 32, 1, 16, 333), (3, 8, 8, 32, 1000), (5, 12, 1, 16, 700),
+                                           (17, 8, 4, 64, 500), (1, 4, 16, 16, 4000), (27, 8, 3, 16, 100)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_of_few_items(n, H, G, ps, most, e4m3):
+    """Around the sizes at which clusters of 8, 4 and 2 blocks take an item, empty sequences among them."""
+    r = np.random.default_rng(n)
+    lens = [most] + r.integers(0, most, n - 1).tolist()
+    if n > 2:
+        lens[1] = 0
+    b = Batch(bt, lens, ps, H, 64, e4m3, seed=n)
+    q = b.queries(n, H * G)
+    qt = torch.from_numpy(q).cuda()
+    for window, sinks in ((0, 0), (100, 7)):
+        status = bt.new_status()
+        out = bt.bwta_attn_decode_paged(qt, b.cache, b.table, 0.125, window, sinks, slots=b.slots, status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        b.check(q, out, [1] * n, 0.125, window, sinks)
+        assert torch.equal(out, bt.bwta_attn_decode_paged(qt, b.cache, b.table, 0.125, window, sinks, slots=b.slots))
+
+
 def test_decode_long_split():
     """One long sequence beside empty and short ones: the length is split over many blocks and joined."""
     lens = [70001, 0, 3, 20000]
