@@ -332,6 +332,9 @@ int bwta_kv_copy_pages(const bwta_kv_cache *src, const bwta_kv_cache *dst, int64
               (i == j && (src[i].k == dst[i].k) != (src[i].v == dst[i].v));
   }
   if (cross) return BWTA_ERR_INVALID_ARG;
+  if (same && (src->num_pages != dst->num_pages || src->page_stride != dst->page_stride ||
+               g.src_sc_stride != g.dst_sc_stride))
+    return BWTA_ERR_INVALID_ARG;  // two descriptions of one pool
   return cuda_status(launch_kv_copy(l, g, same, src_pages, dst_pages, n,
                                     static_cast<int32_t *>(workspace), d_status, (cudaStream_t)stream));
 }

@@ -518,11 +518,11 @@ int bwta_kv_compact(const bwta_kv_cache *caches, int64_t n_layers, const bwta_kv
                     bwta_stream_t stream);
 
 /* Copy page src_pages[i] of every layer of src to page dst_pages[i] of dst (the
- * same geometry, but for num_pages; src and dst may be the same pool). The
- * copies happen at once: refused as BAD_PAGE, without effect, are pages out of
- * range, every copy to a page that the list writes more than once, and, within
- * one pool, every copy from a page that the list writes (other than onto
- * itself).
+ * same geometry, but for num_pages and strides; src and dst are the same pool,
+ * described alike, or share no memory). The copies happen at once: refused as
+ * BAD_PAGE, without effect, are pages out of range, every copy to a page that the
+ * list writes more than once, and, within one pool, every copy from a page that
+ * the list writes (other than onto itself).
  *  src_pages, dst_pages   device int32 [n], n <= BWTA_KV_MAX_POOL
  *  workspace  bwta_kv_pages_workspace(0, n) bytes */
 int bwta_kv_copy_pages(const bwta_kv_cache *src, const bwta_kv_cache *dst, int64_t n_layers,

@@ -177,6 +177,9 @@ def test_page_call_arguments(lib):
     assert copy([cache(v=R)], [cache(v=R + 0x1000)]) == I
     assert copy([cache(v=R)], [cache(k=R, v=P)]) == I
     assert copy([cache(k=P, v=P), cache(k=R, v=R)], [cache(k=R, v=R), cache(k=P, v=P)], layers=2) == I
+    # one pool, described in two ways
+    assert copy([cache(v=R)], [cache(v=R, n=11)]) == I and copy([cache(v=R, n=11)], [cache(v=R)]) == I
+    assert copy([cache(v=R)], [cache(v=R, stride=8192)]) == I
     assert copy([cache()], [cache(k=R, v=R, n=3)], n=0) == bt.BWTA_OK
     assert lib.bwta_kv_pages_workspace(-1, 0) == 0
 
