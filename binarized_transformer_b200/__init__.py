@@ -485,6 +485,8 @@ class KvCache:
 
         def stride(t, inner):
             """Distance of pages; the dimensions inside a page must be dense."""
+            if t.is_contiguous():
+                return inner
             step = 1
             for size, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
                 assert size == 1 or st == step, "the dimensions inside a page must be dense"

@@ -40,10 +40,11 @@
 //
 // Measured on a B200 (a copy moves 6.55 TB/s): fp16, 64 sequences of 0 .. 8191 tokens,
 // 64 query heads on 8 key heads of 128: 1.29 GB in 210 us, 0.94 of the copy's rate;
-// E4M3, 32 sequences, window 4096, 32 heads: 1.10 GB in 200 us, 0.83, bound by the
-// issue of the conversions at 12 warps an SM (45% of the slots; four blocks of 16-token
-// steps 232 us, two of 32-token ones 244); E4M3, one sequence of 250,001 tokens: 0.53 GB
-// in 98 us, 0.82. One token over 333 in fp16, in clusters: 10.7 us, the launch and the
+// E4M3, 32 sequences, window 4096, 32 heads: 1.10 GB in 200 us, 0.83; a longer cache
+// costs 6.2 TB/s more, 0.94, the rest is the start, the ends of items and the last
+// blocks (about 20 us). The arithmetic is hidden (without the second product the time is
+// the same), the warps are not: two blocks an SM 236 us, 16-token steps 241; E4M3, one
+// sequence of 250,001 tokens: 0.53 GB in 96 us, 0.84. One token over 333 in fp16, in clusters: 10.7 us, the launch and the
 // chain length, page, keys, parts.
 #include <algorithm>
 

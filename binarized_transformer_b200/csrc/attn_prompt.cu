@@ -32,14 +32,14 @@
 // of 0 times a NaN would be one). Every wait is bounded; on a
 // timeout the block flags it, lets its copies and MMAs finish, frees TMEM and returns.
 //
-// Measured on a B200: fp16, 2 x 8192 causal tokens, 32 heads of 128: 1.10 TFLOP in 1.19 ms,
-// 925 TFLOP/s, 0.57 of cuBLAS's burst rate (1.37 ms back to back under the power limit).
+// Measured on a B200: fp16, 2 x 8192 causal tokens, 32 heads of 128: 1.10 TFLOP in 1.13 ms,
+// 974 TFLOP/s, 0.60 of cuBLAS's burst rate (1.31 ms back to back under the power limit).
 // An instruction with N = 64 (the scores of a half) takes as long as one with N = 128, 64
-// cycles at best: 48 of them a step and pair, 3070 cycles of the 3960 that it takes. Whole
+// cycles at best: 48 of them a step and pair, 3070 cycles of about 3700 that it takes. Whole
 // 128-key scores (32 instructions a step) leave the tensor cores waiting for the softmax
 // and were slower in each form tried: 1.47 ms in one place, 1.67 with the weights beside
 // them, 1.37 with two threads a row and the tiles taking turns. E4M3, a chunk of 2700 rows
-// at 64 heads on 8 key heads, window 4096: 363 GFLOP in 500 us, 725 TFLOP/s; the
+// at 64 heads on 8 key heads, window 4096: 363 GFLOP in 493 us, 735 TFLOP/s; the
 // conversions add to the issue slots (56% taken).
 #include <algorithm>
 
