@@ -15,8 +15,8 @@
 // rounded to fp16, its sum is not.
 //
 // Warps: 0 and 1 issue the MMAs of tile 0 and 1 (the lowest warps of their SM
-// sub-partitions, which the others' arithmetic then holds up least); then 4 (E4M3: 8)
-// bring keys and values into shared memory (fp16: asynchronous 16-byte copies; E4M3:
+// sub-partitions, which the others' arithmetic then holds up least), 2 fetches Q (TMA);
+// then 4 (E4M3: 8) bring keys and values into shared memory (fp16: asynchronous 16-byte copies; E4M3:
 // bulk copies, converted and scaled, exact in fp16); the last 8 are the softmax of tiles
 // 0 and 1, a thread a row. A step's keys are taken by halves of 64: the scores of the
 // next step's half are computed as soon as this one's weights, which overwrite the
@@ -272,7 +272,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 template <int DP, bool E4M3>
-__global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const PrArgs A) {
+__global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const __grid_constant__ CUtensorMap map_q, const PrArgs A) {
   using S = PrShape<DP, E4M3>;
   using W = PrWarps<E4M3>;
   extern __shared__ uint8_t smem_raw[];
@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       mbar_init(&bars->full[i], W::LOAD);
       mbar_init(&bars->empty[i], 2);
     }
-    mbar_init(&bars->q_ready, 8);
+    mbar_init(&bars->q_ready, 1);
+    prefetch_tensormap(&map_q);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_ready[i][0], 1);
       mbar_init(&bars->s_ready[i][1], 1);
@@ -305,6 +306,11 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
   }
   if (D % 16 != 0) {  // the products read 8 columns past D, which are never written: zero once
     for (int i = threadIdx.x * 16; i < (2 + S::SLOTS) * S::TILE; i += W::THREADS * 16)
+      *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (A.R * A.group < PR_T) {  // rows that the copies of Q leave out
+    for (int i = threadIdx.x * 16; i < 2 * S::TILE; i += W::THREADS * 16)
       *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -328,26 +334,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
     const int w = (warp - W::SOFTMAX0) / 4, q = warp % 4, r = q * 32 + lane;
     if (it.live) {
       const int chunks = D / 8;
-      // Q rows of this tile, into the layout of the keys
       uint8_t *qs = base + w * S::TILE;
       const int used = it.cnt[w] * A.group;
-      const uint16_t *src = a.q + (it.row0 + (int64_t)w * A.R) * a.ldq + (int64_t)it.head * A.group * D;
       const uint32_t by_chunks = 65536u / chunks + 1, by_group = 65536u / A.group + 1;  // exact below 2048
-#pragma unroll 1
-      for (int p = threadIdx.x % 128; p < PR_T * chunks; p += 128) {
-        const int rr = (int)((p * by_chunks) >> 16), c = p - rr * chunks, i = (int)((rr * by_group) >> 16);
-        const bool in = rr < used;
-        const uint16_t *from = in ? src + (int64_t)i * a.ldq + (int64_t)(rr - i * A.group) * D + c * 8 : a.q;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         smem_addr(qs) + (c / 8) * (PR_T * 128) + swz128(rr, c % 8)),
-                     "l"(from), "r"(in ? 16 : 0)
-                     : "memory");
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_ready);
-
       const int tok = r / A.group;
       const int p = it.pmin[w] + tok;
       const bool valid = r < used;
@@ -706,6 +695,17 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
   } else {
     // ------------------------------------------------ MMA issue
     regs_dec<W::REG_MMA>();
+    // warp 2: the rows of Q, R tokens of G heads, into the layout of the keys (rows past the
+    // tile's are other tokens' and do not count)
+    if (warp == 2 && lane == 0 && steps > 0) {
+      const uint32_t bytes = 128 * A.R * A.group;
+      const int tiles = it.cnt[1] > 0 ? 2 : 1;
+      mbar_arrive_expect_tx(&bars->q_ready, tiles * S::NH * bytes);
+      for (int i = 0; i < tiles * S::NH; ++i)
+        tma_load_3d(base + i / S::NH * S::TILE + i % S::NH * (PR_T * 128), &map_q, i % S::NH * 64,
+                    it.head * A.group, (int32_t)it.row0 + i / S::NH * A.R, &bars->q_ready);
+      if (!mbar_wait(&bars->q_ready, 0)) bars->timeout = bars->undrained = 1;
+    }
     // warp w issues the products of tile w, all lanes in step
     if (warp < 2 && steps > 0) {
       const int w = warp, n = __shfl_sync(FULL, steps, 0);
@@ -860,13 +860,29 @@ int64_t attn_prompt_blocks(int64_t n_seq, int64_t total_q, int64_t n_heads, int6
   return n_kv_heads * (total_q / two + std::min(n_seq, total_q));  // a sum of rounded-up quotients at most
 }
 
+// Q as [total_q][n_heads][D]; a box is 64 columns of a tile's tokens and heads.
+static bool make_q_map(CUtensorMap *map, const PrArgs &A) {
+  PFN_encodeTiled enc = get_encode_tiled();
+  if (!enc) return false;
+  const AttnArgs &a = A.a;
+  cuuint64_t dims[3] = {(cuuint64_t)a.c.D, (cuuint64_t)a.n_heads, (cuuint64_t)a.total_q};
+  cuuint64_t strides[2] = {(cuuint64_t)a.c.D * 2, (cuuint64_t)a.ldq * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)A.group, (cuuint32_t)A.R};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t *>(a.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP, bool E4M3>
 static cudaError_t launch_prompt_t(const PrArgs &A, int64_t blocks, cudaStream_t s) {
   static SmemOptIn opt_in;
   auto kern = k_attn_prompt<DP, E4M3>;
   if (cudaError_t e = opt_in(kern, PrShape<DP, E4M3>::SMEM)) return e;
+  CUtensorMap map;
+  if (!make_q_map(&map, A)) return cudaErrorInvalidValue;
   return launch_pdl_cluster(kern, dim3((unsigned)(blocks * A.split)), (unsigned)A.split, dim3(PrWarps<E4M3>::THREADS),
-                            PrShape<DP, E4M3>::SMEM, s, A);
+                            PrShape<DP, E4M3>::SMEM, s, map, A);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {

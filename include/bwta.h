@@ -461,7 +461,7 @@ int64_t bwta_attn_decode_workspace(int64_t n_heads, int64_t n_kv_heads, int64_t 
  * values are in the pages already: row i of sequence s's n rows is the query at
  * position kv_len - n + i (a whole prompt when n = kv_len, a chunk of one
  * otherwise). A row at a negative position sees nothing and gives zeros. Rows
- * at and past cu_q[n_seq] are neither read nor written.
+ * at and past cu_q[n_seq] have no influence and are not written.
  *  cu_q     int32 [n_seq+1] ascending, first 0, last <= total_q
  *  q, out   fp16 [total_q][n_heads * head_dim]
  *  Limits: n_heads / n_kv_heads <= 128.
