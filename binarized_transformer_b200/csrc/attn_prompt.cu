@@ -432,9 +432,10 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
       }
       // output
       bool finite = true;
-      // (the shared memory of keys and values is free once both tiles' products are done)
+      // (for a share, which goes where the keys and values are, both tiles' products)
       if (steps > 0 && ok)
-        ok = __all_sync(FULL, pr_wait(bars, &bars->o_done[w], 0) && pr_wait(bars, &bars->o_done[1 - w], 0));
+        ok = __all_sync(FULL, pr_wait(bars, &bars->o_done[w], 0) &&
+                                  (it.parts == 1 || pr_wait(bars, &bars->o_done[1 - w], 0)));
       if (ok && it.parts > 1 && steps > 0) {
         // a share: for the cluster to add up
         tc_fence_after();
