@@ -767,8 +767,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
     last = cut.owner(u + q.units - 1);
     row = h - kh * heads - hg * A.per_item;
   }
+  // No early trigger: blocks of the next kernel that wait here already would take the
+  // places of this one's (64 ragged sequences, call after call: 237 us for 211).
   pdl_wait();
-  pdl_trigger();
   if (h >= a.n_heads) return;
   uint16_t *out = a.out + s * a.ldo + (int64_t)h * D + lane * 4;
   if (q.units == 0) {
