@@ -696,8 +696,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
   }
   cp_wait<0>();
   if (CLUSTER) {
-    if (n == 0 && threadIdx.x < ROWS)
-      *reinterpret_cast<float2 *>(joint + threadIdx.x * (DP + 2) + DP) = make_float2(-INFINITY, 0.0f);
+    if (n == 0 && threadIdx.x < ROWS)  // no tile: a sum that no weights have says so
+      *reinterpret_cast<float2 *>(joint + threadIdx.x * (DP + 2) + DP) = make_float2(-INFINITY, -1.0f);
     __syncwarp();
     cluster_sync();
     // each block adds up some rows: a warp a row, 4 columns a lane
@@ -709,8 +709,9 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
       for (int k = 0; k < A.cluster; ++k) M = fmaxf(M, cluster_ld2(part + (row * (DP + 2) + DP) * 4, k).x);
       for (int k = 0; k < A.cluster; ++k) {
         const float2 ml = cluster_ld2(part + (row * (DP + 2) + DP) * 4, k);
-        if (ml.x == -INFINITY) continue;  // no visible key there
-        const float f = exp2_fast(ml.x - M);
+        if (ml.y == -1.0f) continue;
+        // no score above -infinity there: the sums are zeros, or the NaN that the output has to show
+        const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - M);
         L += ml.y * f;
         if (lane * 4 < D) {
           const float2 v0 = cluster_ld2(part + (row * (DP + 2) + lane * 4) * 4, k);
