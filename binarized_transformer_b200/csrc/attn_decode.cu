@@ -3,8 +3,8 @@
 //
 // For every query head, o = sum_j w_j v_j / sum_j w_j with w_j = 2^(x_j - m) and
 // x_j = softmax_scale * log2(e) * (q . k_j). The keys and values are read once:
-// m, l = sum w and the weighted sum of the values are running values, rescaled
-// by 2^(m_old - m_new) when the maximum grows. Two halves of the keys joined:
+// m (near the maximum of x), l = sum w and the weighted sum of the values are running
+// values, rescaled by 2^(m_old - m_new) when m grows. Two halves of the keys joined:
 // m = max(m_a, m_b), l = l_a 2^(m_a - m) + l_b 2^(m_b - m), the same for the sums.
 //
 // Work: an item is a sequence's key head with up to 16 of its query heads, its
@@ -32,9 +32,9 @@
 // the running sums of 8 heads take 32 registers. The fifth-generation instructions
 // would need 64 or 128 rows, and here HBM is the bound: 23 bytes a clock and SM.
 //
-// The reference m follows the maximum only when a score passes it by 2^8 (weights
-// up to 2^8 are kept): most tiles then need no maximum over the lanes. P is rounded
-// to fp16 for the second product, l sums it unrounded. E4M3: K's scale is applied
+// The reference m starts 7 below the maximum and follows it only when a score passes it
+// by 15 (ATTN_HEAD, ATTN_SLACK): most tiles then need no maximum over the lanes. P is
+// rounded to fp16 for the second product, l sums it unrounded. E4M3: K's scale is applied
 // to the scores in fp32; V's, a power of two, to the converted values, which stays
 // exact.
 //
@@ -56,7 +56,6 @@ namespace bwta {
 constexpr int DEC_WARPS = 4, DEC_THREADS = DEC_WARPS * 32;
 constexpr int DEC_MAX_ROWS = 16;  // query heads of an item at most
 constexpr int DEC_MAX_BLOCKS = 640;
-constexpr float DEC_SLACK = 8.0f;  // how far scores may pass the reference (log2)
 constexpr int JOIN_THREADS = 256, JOIN_HEADS = JOIN_THREADS / 32;
 
 __host__ __device__ constexpr int dec_tile(bool e4m3) { return e4m3 ? 128 : 64; }
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
         for (int e = 0; e < 2; ++e) {
           float x = fmaxf(s[0][b][e], s[0][b][2 + e]);
           if (MT == 2) x = fmaxf(fmaxf(x, s[MT - 1][b][e]), s[MT - 1][b][2 + e]);
-          up |= x > m[b][e] + DEC_SLACK;  // also from -infinity
+          up |= x > m[b][e] + ATTN_SLACK;  // also from -infinity
         }
       if (__any_sync(FULL, up)) {
 #pragma unroll
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
             if (MT == 2) x = fmaxf(fmaxf(x, s[MT - 1][b][e]), s[MT - 1][b][2 + e]);
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(FULL, x, d));
-            const float mn = fmaxf(m[b][e], x);
+            const float mn = fmaxf(m[b][e], x - ATTN_HEAD);
             // nothing seen so far: the sums are zero and the factor does not matter
             const float f = m[b][e] == -INFINITY ? 0.0f : exp2_fast(m[b][e] - mn);
             m[b][e] = mn;

@@ -9,9 +9,9 @@
 // and walks their visible key tiles of 128 tokens; the tensor cores work on one
 // tile's products while the other tile's softmax runs.
 //
-// The running reference m of a row follows its maximum only when a score passes it
-// by more than 2^8: until then weights up to 2^8 (of fp16's 2^16) are kept, and
-// the output in TMEM does not have to be rescaled. Sums and outputs are fp32; P is
+// The running reference m of a row starts 7 below its maximum and follows it only when a
+// score passes it by more than 15 (ATTN_HEAD, ATTN_SLACK): until then weights up to 2^15 (of
+// fp16's 2^16) are kept, and the output in TMEM does not have to be rescaled. Sums and outputs are fp32; P is
 // rounded to fp16, its sum is not.
 //
 // Warps: 0 and 1 issue the MMAs of tile 0 and 1 (the lowest warps of their SM
@@ -70,7 +70,6 @@ struct PrWarps {
 constexpr int PR_LAG = 1;
 constexpr int PR_HALF = 64;         // keys of one product (scores and weights)
 constexpr int PR_MIN_STEPS = 2;     // key tiles that are worth a block of their own
-constexpr float PR_SLACK = 8.0f;    // how far scores may pass the reference (log2)
 template <int DP, bool E4M3>
 struct PrShape {
   static constexpr int NH = DP / 64;                  // halves of 64 columns
@@ -385,9 +384,9 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
               top[c] = fmaxf(fmaxf(top[c], __uint_as_float(v[c / 2][i + (c % 2) * 2])),
                              __uint_as_float(v[c / 2][i + (c % 2) * 2 + 1]));
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
-          const bool up = mx > m + PR_SLACK || (m == -INFINITY && mx > m);
+          const bool up = mx > m + ATTN_SLACK;  // also from -infinity
           if (__any_sync(FULL, up)) {
-            const float mn = up ? mx : m;
+            const float mn = up ? mx - ATTN_HEAD : m;
             // nothing seen so far: the sums are zero and the factor does not matter
             const float f = m == -INFINITY ? 0.0f : pr_exp2(m - mn);
             m = mn;

@@ -10,6 +10,15 @@ namespace bwta {
 
 constexpr int KV_MAX_D = 128;
 
+// The softmax's weights are 2^(x - m), rounded to fp16 for the product with V. The
+// reference m is set ATTN_HEAD below the maximum seen so far and follows it when a
+// score passes m by more than ATTN_SLACK (log2), so the weights use all of fp16's
+// range: up to 2^15, and down to 2^-21 of the largest before they lose bits and 2^-32
+// before they vanish. (With m at the maximum the small weights of a long row behind
+// one dominant key were lost while their sum counted them: 32,768 keys behind a first
+// one of 99.9% of the weight, the output off by a third.)
+constexpr float ATTN_HEAD = 7.0f, ATTN_SLACK = 15.0f;
+
 // One layer's pool. Strides in elements of k / v and in floats of the scales.
 struct KvView {
   const uint8_t *k, *v;

@@ -432,8 +432,9 @@ int bwta_kv_append(const bwta_kv_cache *cache, const bwta_kv_table *table, const
  * over the visible keys: j <= p, and with window > 0 also j > p - window or
  * j < sinks. An empty slot gives zeros. Scores, maxima, sums and the weighted
  * sum are fp32; the weights are rounded to fp16 before they meet V (their sum
- * takes them unrounded), and o is rounded to fp16 once. (In place of the maximum
- * the kernels use a value at most 8 log 2 below it: weights up to 256.)
+ * takes them unrounded), and o is rounded to fp16 once. In place of the maximum
+ * the kernels use a value 7 log 2 to 15 log 2 below it: a weight of less than
+ * 2^-21 of the largest is held in steps of 2^-31 of it.
  *  q        fp16 [n_seq][n_heads * head_dim], rows ldq elements apart
  *  out      fp16 [n_seq][n_heads * head_dim], rows ldo elements apart
  *  window   0 = every key, else >= 1; sinks >= 0 (only with a window)

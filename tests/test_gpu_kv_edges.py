@@ -88,3 +88,119 @@ def test_newest_key_alone_in_its_share_is_nan(length, window, sinks, rows, e4m3)
     one = Batch.__new__(Batch)                                # the other key head's queries are as ever
     one.H, one.D, one.lens, one.k, one.v = 1, 64, b.lens, [b.k[0][:1]], [b.v[0][:1]]
     one.check(q[:, :3], out[:, :3], [1], 0.125, window, sinks)
+
+
+# ------------------------------------------------------------------ weights of unlike sizes
+def attend_tight(q, k, v, p, scale, window=0, sinks=0):
+    """One query row at position p against 64 bits: (o [D], bound [D]).
+
+    With w the weights over their sum, A = sum w |v|, n keys, fp16's half step 2^-11 and fp32's 2^-24:
+    * a weight is rounded to fp16. The largest one is held as at least 2^7 (the reference is 7 below the
+      maximum), so a weight is normal down to 2^-21 of the largest and rounded by 2^-11 of itself; below,
+      by half a subnormal step, 2^-25 / 2^7 of the largest, and by no more than itself
+    * a score is an fp32 sum of D products and the exponent's multiplication and subtraction: an absolute
+      error d, a relative one of each weight, met by the weights and by their sum; exp2 within 2^-22
+    * the sums run in fp32: at most n / 16 steps of the products, whose additions may cut instead of
+      round (2^-23 of the sum so far, at most A), and n / 32 + 64 additions of the weights (2^-24)
+    * the result is rounded to fp16: 2^-11 of it, or half the smallest step, 2^-25"""
+    j = np.arange(min(len(k), p + 1))
+    if window:
+        j = j[(j > p - window) | (j < sinks)]
+    x = (k[j] @ q) * scale
+    w = np.exp(x - x.max())
+    w /= w.sum()
+    o, a, n = w @ v[j], w @ np.abs(v[j]), len(j)
+    d = (k.shape[1] + 2) * 2.0 ** -24 * scale * (np.abs(k[j]) @ np.abs(q)).max() + 2.0 ** -22 * np.abs(x).max()
+    per_key = np.minimum(w, np.maximum(2.0 ** -11 * w, 2.0 ** -32 * w.max())) @ np.abs(v[j])
+    sums = n / 16 * 2.0 ** -23 + (n / 32 + 64) * 2.0 ** -24
+    return o, 2.0 ** -11 * np.abs(o) + 2.0 ** -25 + per_key + (2 * d + 2.0 ** -21 + sums) * a
+
+
+def check_tight(b, q, out, seqs, positions, scale, window=0, sinks=0, rows=None):
+    """Rows of q, out [n, heads, D]: row i is sequence seqs[i]'s query at positions[i]."""
+    got, g, worst = out.cpu().double().numpy(), q.shape[1] // b.H, 0.0
+    pick = range(len(q)) if rows is None or len(q) <= rows else np.unique(np.linspace(0, len(q) - 1, rows).astype(int))
+    for i in pick:
+        for h in range(q.shape[1]):
+            o, bound = attend_tight(q[i, h].astype(np.float64), b.k[seqs[i]][h // g], b.v[seqs[i]][h // g], positions[i],
+                                    scale, window, sinks)
+            err = np.abs(got[i, h] - o)
+            assert (err <= bound).all(), (i, h, float(np.nanmax(err / bound)))
+            worst = max(worst, float((err / bound).max()))
+    return worst
+
+
+@pytest.mark.parametrize("call", ["decode", "decode_cluster", "prompt", "prompt_cluster"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_dominant_first_token_and_a_long_tail(call, D, e4m3):
+    """A sink takes 99.9% of the weight and its value is zero: the output is the tail's, weights of 2^-25 of
+    the largest each. Many rows, so that one block walks a whole sequence, or few, which share one."""
+    t = 3500 if call == "decode_cluster" else 32768
+    b = Batch(bt, [t], 64, 1, D, e4m3, seed=D)
+    k, v = b.k[0].copy(), b.v[0].copy()
+    k[0, :, 0] = 0.0
+    k[0, 0] = 0.0
+    k[0, 0, 0] = 64.0
+    v[0, 0] = 0.0
+    put(b, 0, k, v)
+    n = {"decode": 450, "decode_cluster": 1, "prompt": 150, "prompt_cluster": 3}[call]
+    q = b.queries(n, 1, size=(64.0 / D) ** 0.5)
+    scale = 0.125
+    tail = math.log(t) + 0.5                                  # log of the sum of weights with scores of variance 1
+    q[:, :, 0] = (tail + math.log(999.0)) / (64.0 * scale)
+    slots = b.slots.repeat(n)
+    status = bt.new_status()
+    qt = torch.from_numpy(q).cuda()
+    if call.startswith("decode"):
+        table = b.table if call == "decode_cluster" else long_rows(b)
+        out = bt.bwta_attn_decode_paged(qt, b.cache, table, scale, slots=slots, status=status)
+    else:
+        out = bt.bwta_attn_prompt_paged(qt, cu(list(range(n + 1))), b.cache, b.table, scale, slots=slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    check_tight(b, q, out, [0] * n, [t - 1] * n, scale, rows=8)
+
+
+@pytest.mark.parametrize("rows", ["short", "long"])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_every_unit_of_a_long_sequence_counts(rows, e4m3):
+    """Scores next to equal, V marks the unit of 64 tokens (column c: units c, c + D, ...): a unit lost or
+    counted twice at a cut changes a column by more than a twentieth."""
+    lens = [70001, 0, 3, 20000] if rows == "long" else [4000, 0, 3, 2900]
+    b = Batch(bt, lens, 64, 2, 64, e4m3, seed=6)
+    for s, t in enumerate(lens):
+        if t:
+            mark = (np.arange(t)[:, None] // 64 % 64 == np.arange(64)).astype(np.float64)
+            put(b, s, v=np.broadcast_to(mark, (2, t, 64)).copy())
+    q = b.queries(4, 8, size=0.1)
+    qt = torch.from_numpy(q).cuda()
+    status = bt.new_status()
+    table = b.table if rows == "short" else long_rows(b)
+    picks = [0, 2, 3]
+    for window, sinks in ((0, 0), (1700, 129)):
+        out = bt.bwta_attn_decode_paged(qt, b.cache, table, 0.125, window, sinks, slots=b.slots, status=status)
+        assert (out[1] == 0).all()
+        check_tight(b, q[picks], out[picks], picks, [lens[s] - 1 for s in picks], 0.125, window, sinks)
+        out = bt.bwta_attn_prompt_paged(qt, cu([0, 1, 2, 3, 4]), b.cache, table, 0.125, window, sinks, slots=b.slots,
+                                        status=status)
+        assert (out[1] == 0).all()
+        check_tight(b, q[picks], out[picks], picks, [lens[s] - 1 for s in picks], 0.125, window, sinks)
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_every_unit_of_a_long_prompt_counts(e4m3):
+    """The same for many rows of a prompt, each of which sees another number of keys."""
+    t, n = 9000, 3000
+    b = Batch(bt, [t], 64, 2, 64, e4m3, seed=7)
+    mark = (np.arange(t)[:, None] // 64 % 64 == np.arange(64)).astype(np.float64)
+    put(b, 0, v=np.broadcast_to(mark, (2, t, 64)).copy())
+    q = b.queries(n, 4, size=0.1)
+    qt = torch.from_numpy(q).cuda()
+    for window, sinks in ((0, 0), (1700, 129)):
+        status = bt.new_status()
+        out = bt.bwta_attn_prompt_paged(qt, cu([0, n]), b.cache, b.table, 0.125, window, sinks, slots=b.slots, status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        check_tight(b, q, out, [0] * n, list(range(t - n, t)), 0.125, window, sinks, rows=60)
