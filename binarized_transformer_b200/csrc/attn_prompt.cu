@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
         *reinterpret_cast<float2 *>(base + (w * PR_T + r) * 8) = make_float2(m, l);
       } else if (ok && blockIdx.x % A.split == 0) {
         tc_fence_after();
-        const bool none = !(l > 0.0f || l != l);  // a row that sees nothing: zeros
+        const bool none = p < 0;  // sees nothing: zeros (from p = 0 on a row sees a key)
         const float inv = 1.0f / l;
         float zero = 0.0f;  // stays 0 unless an output is not finite
         // through shared memory (Q has been read), so that rows are written whole
@@ -827,15 +827,16 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
           y.w += x.w * f;
         }
         if (lane * 4 < D) {
-          const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+          const int tok = r / A.group;
+          const bool none = it.pmin[w] + tok < 0;  // sees nothing: zeros
+          const float inv = 1.0f / L;
           float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            z[e] = inv == 0.0f ? 0.0f : z[e] * inv;
+            z[e] = none ? 0.0f : z[e] * inv;
             finite &= z[e] - z[e] == 0.0f;
           }
           const __half2 a2 = __floats2half2_rn(z[0], z[1]), b2 = __floats2half2_rn(z[2], z[3]);
-          const int tok = r / A.group;
           uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R + tok) * a.ldo +
                           ((int64_t)it.head * A.group + (r - tok * A.group)) * D;
           *reinterpret_cast<uint2 *>(out + lane * 4) =

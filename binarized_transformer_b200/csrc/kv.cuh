@@ -15,8 +15,8 @@ constexpr int KV_MAX_D = 128;
 // score passes m by more than ATTN_SLACK (log2), so the weights use all of fp16's
 // range: up to 2^15, and down to 2^-21 of the largest before they lose bits and 2^-32
 // before they vanish. (With m at the maximum the small weights of a long row behind
-// one dominant key were lost while their sum counted them: 32,768 keys behind a first
-// one of 99.9% of the weight, the output off by a third.)
+// one dominant key are lost while their sum counts them: of 32,768 keys behind a first
+// one with 99.9% of the weight and no value, a fifth of the output.)
 constexpr float ATTN_HEAD = 7.0f, ATTN_SLACK = 15.0f;
 
 // One layer's pool. Strides in elements of k / v and in floats of the scales.

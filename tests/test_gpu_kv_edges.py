@@ -204,3 +204,29 @@ def test_every_unit_of_a_long_prompt_counts(e4m3):
         torch.cuda.synchronize()
         assert status.item() == 0
         check_tight(b, q, out, [0] * n, list(range(t - n, t)), 0.125, window, sinks, rows=60)
+
+
+# ------------------------------------------------------------------ scores of minus infinity
+@pytest.mark.parametrize("t,n", [(40, 40), (300, 7), (5000, 3)])
+def test_rows_whose_every_score_is_minus_infinity(t, n):
+    """0 / 0 is not the zero of a row that sees nothing: NaN, and flagged, by both calls."""
+    b = Batch(bt, [t], 16, 2, 64)
+    q = np.abs(b.queries(n + 2, 4)) + np.float16(0.5)
+    b.cache.k[:, 1, :, 5] = -math.inf                         # key head 1
+    b.table.kv_len[b.slots.long()] = t
+    qt = torch.from_numpy(q).cuda()
+    status = bt.new_status()
+    # two rows more than the sequence has when n = t: these see nothing
+    out = bt.bwta_attn_prompt_paged(qt, cu([0, n + 2]), b.cache, b.table, 0.125, slots=b.slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == bt.STATUS_NONFINITE
+    blind = max(0, n + 2 - t)
+    assert (out[:blind] == 0).all() and torch.isnan(out[blind:, 2:]).all()
+    one = Batch.__new__(Batch)
+    one.H, one.D, one.lens, one.k, one.v = 1, 64, b.lens, [b.k[0][:1]], [b.v[0][:1]]
+    one.check(q[blind:, :2], out[blind:, :2], [n + 2 - blind], 0.125, rows=8)
+    status.zero_()
+    out = bt.bwta_attn_decode_paged(qt[:1], b.cache, b.table, 0.125, slots=b.slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == bt.STATUS_NONFINITE and torch.isnan(out[:, 2:]).all()
+    one.check(q[:1, :2], out[:, :2], [1], 0.125)
