@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
         for (int e = 0; e < 2; ++e) {
           float x = fmaxf(s[0][b][e], s[0][b][2 + e]);
           if (MT == 2) x = fmaxf(fmaxf(x, s[MT - 1][b][e]), s[MT - 1][b][2 + e]);
-          up |= x > m[b][e] + ATTN_SLACK;  // also from -infinity
+          up |= x - m[b][e] > ATTN_SLACK;  // also from -infinity; m + slack could be rounded up to x
         }
       if (__any_sync(FULL, up)) {
 #pragma unroll

@@ -230,3 +230,85 @@ def test_rows_whose_every_score_is_minus_infinity(t, n):
     torch.cuda.synchronize()
     assert status.item() == bt.STATUS_NONFINITE and torch.isnan(out[:, 2:]).all()
     one.check(q[:1, :2], out[:, :2], [1], 0.125)
+
+
+# ------------------------------------------------------------------ scores past what fp32 resolves
+LN2 = float(np.float32(math.log(2.0)))                        # softmax_scale * log2(e) is 1 in fp32
+
+
+def one_hot_queries(n, heads, D, cols):
+    q = np.zeros((n, heads, D), np.float16)
+    for c, x in cols.items():
+        q[:, :, c] = x
+    return q
+
+
+@pytest.mark.parametrize("call", ["decode", "decode_long", "prompt", "prompt_cluster"])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_scores_of_millions_and_billions(call, e4m3):
+    """fp16's largest queries and keys: one key takes all, wherever it lies. One product a score, so the scores
+    are exact in fp32, and the keys' differ by 10^5 at least. The prompt call takes scores up to 2^27; beyond, a
+    row is NaN and flagged."""
+    t = 700
+    b = Batch(bt, [t], 16, 1, 64, e4m3)
+    table = b.table if call in ("decode", "prompt_cluster") else long_rows(b)
+    n = {"prompt": 200, "decode_long": 450}.get(call, 1)      # many rows: one block walks a whole sequence
+    for scale in (0.0011, 0.035, 0.37, 1.0):
+        for top in (0, 77, 128, 699):
+            for sign in (1.0, -1.0):
+                k = np.zeros((1, t, 64))
+                k[0, :, 3] = np.where(np.arange(t) == top, 57344.0, 53248.0 - 4096.0 * (np.arange(t) % 5))
+                if sign < 0:                                  # all scores far below zero
+                    k[0, :, 3] = -np.where(np.arange(t) == top, 36864.0, 40960.0 + 4096.0 * (np.arange(t) % 5))
+                put(b, 0, k)
+                q = one_hot_queries(n, 2, 64, {3: 65504.0})
+                qt = torch.from_numpy(q).cuda()
+                status = bt.new_status()
+                slots = b.slots.repeat(n)
+                if call.startswith("decode"):
+                    out = bt.bwta_attn_decode_paged(qt, b.cache, table, scale, slots=slots, status=status)
+                else:
+                    out = bt.bwta_attn_prompt_paged(qt, cu(list(range(n + 1))), b.cache, table, scale, slots=slots,
+                                                    status=status)
+                torch.cuda.synchronize()
+                if call.startswith("prompt") and scale > 0.1:
+                    assert status.item() == bt.STATUS_NONFINITE and torch.isnan(out).all(), (scale, top, sign)
+                    continue
+                want = b.v[0][0, top]
+                # the largest weight is rounded to fp16 and the sum is not; the result is rounded to fp16
+                bound = (2.0 ** -10 + 2.0 ** -20) * np.abs(want) + 2.0 ** -25
+                err = np.abs(out.cpu().double().numpy() - want)
+                assert status.item() == 0, (scale, top, sign)
+                assert (err <= bound).all(), (scale, top, sign)
+
+
+@pytest.mark.parametrize("call", ["decode", "prompt"])
+def test_steps_of_the_score_around_the_slack(call):
+    """Scores of 2^27 + 16 r (exact, fp32's own steps there are 16): the next tile's maximum passes the
+    reference by 16 = 2^16 of a weight, more than fp16 holds."""
+    t, n = 512, 450                                           # many rows: one block walks a whole sequence
+    for r0 in (1, 2, 3, 4):
+        b = Batch(bt, [t], 16, 1, 64)
+        k = np.zeros((1, t, 64))
+        k[0, :, 0] = 8192.0
+        k[0, :, 1] = r0 + np.arange(t) // 64                  # one more in each 64 tokens
+        k[0, :, 1] += np.arange(t) % 64 == 63
+        k[0, 64:, 1] -= 1
+        put(b, 0, k)
+        q = one_hot_queries(n, 1, 64, {0: 16384.0, 1: 16.0})
+        qt = torch.from_numpy(q).cuda()
+        status = bt.new_status()
+        slots = b.slots.repeat(n)
+        if call == "decode":
+            out = bt.bwta_attn_decode_paged(qt, b.cache, long_rows(b), LN2, slots=slots, status=status)
+        else:
+            out = bt.bwta_attn_prompt_paged(qt, cu(list(range(n + 1))), b.cache, b.table, LN2, slots=slots, status=status)
+        torch.cuda.synchronize()
+        x = 16.0 * k[0, :, 1]
+        w = 2.0 ** (x - x.max())
+        w /= w.sum()
+        o, a = w @ b.v[0][0], w @ np.abs(b.v[0][0])
+        # scores and their differences are exact; weights, exp2, sums and the result are rounded
+        bound = 2.0 ** -11 * np.abs(o) + 2.0 ** -25 + (2.0 ** -11 + 2.0 ** -20) * a + t * 2.0 ** -32 * 4
+        assert status.item() == 0, r0
+        assert (np.abs(out[:, 0].cpu().double().numpy() - o) <= bound).all(), r0
