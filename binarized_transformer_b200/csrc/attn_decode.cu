@@ -667,23 +667,24 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
             const float inv = 1.0f / l[b][e];
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              const float y0 = o[b][ks][e], y1 = o[b][ks][2 + e];
+              const float y0 = o[b][ks][e], y1 = o[b][ks][2 + e];  // sums, and means of them
+              const float z0 = mean_to_f16_range(y0 * inv), z1 = mean_to_f16_range(y1 * inv);
               const int c0 = ks * 16 + (E4M3 ? 2 * g : g), c1 = c0 + (E4M3 ? 1 : 8);
               if (E4M3) {  // two neighbours
                 if (c0 >= D) continue;
-                if (whole) *reinterpret_cast<uint32_t *>(out + c0) = half2_bits(y0 * inv, y1 * inv);
+                if (whole) *reinterpret_cast<uint32_t *>(out + c0) = half2_bits(z0, z1);
                 else *reinterpret_cast<float2 *>(piece + c0) = make_float2(y0, y1);
-                if (whole) finite &= y0 * inv - y0 * inv == 0.0f && y1 * inv - y1 * inv == 0.0f;
+                if (whole) finite &= z0 - z0 == 0.0f && z1 - z1 == 0.0f;
               } else {
                 if (c0 < D) {
-                  if (whole) out[c0] = __half_as_ushort(__float2half_rn(y0 * inv));
+                  if (whole) out[c0] = __half_as_ushort(__float2half_rn(z0));
                   else piece[c0] = y0;
-                  if (whole) finite &= y0 * inv - y0 * inv == 0.0f;
+                  if (whole) finite &= z0 - z0 == 0.0f;
                 }
                 if (c1 < D) {
-                  if (whole) out[c1] = __half_as_ushort(__float2half_rn(y1 * inv));
+                  if (whole) out[c1] = __half_as_ushort(__float2half_rn(z1));
                   else piece[c1] = y1;
-                  if (whole) finite &= y1 * inv - y1 * inv == 0.0f;
+                  if (whole) finite &= z1 - z1 == 0.0f;
                 }
               }
             }
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
         const float inv = at.q.units ? 1.0f / L : 0.0f;  // an empty sequence: zeros
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[e] *= inv;
+          y[e] = mean_to_f16_range(y[e] * inv);
           finite &= y[e] - y[e] == 0.0f;
         }
         *reinterpret_cast<uint2 *>(a.out + at.s * a.ldo + (int64_t)(kh * heads + h0 + row) * D + lane * 4) =
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
   bool finite = true;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    y[e] /= L;
+    y[e] = mean_to_f16_range(y[e] / L);
     finite &= y[e] - y[e] == 0.0f;
   }
   if (col) {

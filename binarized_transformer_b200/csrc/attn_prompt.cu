@@ -248,6 +248,14 @@ __device__ __forceinline__ float pr_exp2(float x) {
   return y;
 }
 
+// Two numbers as halves, those past fp16's range as +-65504 (NaN stays). Rounded weights
+// over the sum of unrounded ones make means up to 2^-11 larger than the largest value.
+__device__ __forceinline__ uint32_t pr_half2_limited(float x, float y) {
+  uint32_t h;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  return h;
+}
+
 // Two fp32 numbers in a register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pk2(float x, float y) {
   uint64_t r;
@@ -478,8 +486,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
               const float x = none ? 0.0f : __uint_as_float(o[i * 8 + 2 * e]) * inv;
               const float y = none ? 0.0f : __uint_as_float(o[i * 8 + 2 * e + 1]) * inv;
               if (c * 32 + i * 8 < D) zero = fmaf(x, 0.0f, fmaf(y, 0.0f, zero));
-              const __half2 two = __floats2half2_rn(x, y);
-              h[e] = *reinterpret_cast<const uint32_t *>(&two);
+              h[e] = pr_half2_limited(x, y);
             }
             const int cc = c * 4 + i;
             *reinterpret_cast<uint4 *>(qs + (cc / 8) * (PR_T * 128) + swz128(r, cc % 8)) =
@@ -487,6 +494,14 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
           }
         }
         finite = !valid || zero == 0.0f;
+        if (!finite) {  // the limit has taken Inf too: +-65504 in this row is Inf again
+#pragma unroll 1
+          for (int i = 0; i < chunks * 4; ++i) {
+            uint32_t *h = reinterpret_cast<uint32_t *>(qs + (i / 32) * (PR_T * 128) + swz128(r, i / 4 % 8)) + i % 4;
+            *h += (*h & 0x7fffu) == 0x7bffu;
+            *h += (*h & 0x7fff0000u) == 0x7bff0000u ? 0x10000u : 0u;
+          }
+        }
         __syncwarp();
         uint16_t *out = a.out + (it.row0 + (int64_t)w * A.R) * a.ldo + (int64_t)it.head * A.group * D;
 #pragma unroll 4
@@ -838,7 +853,7 @@ __global__ void __launch_bounds__(PrWarps<E4M3>::THREADS, 1) k_attn_prompt(const
           float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            z[e] = none ? 0.0f : z[e] * inv;
+            z[e] = none ? 0.0f : mean_to_f16_range(z[e] * inv);
             finite &= z[e] - z[e] == 0.0f;
           }
           const __half2 a2 = __floats2half2_rn(z[0], z[1]), b2 = __floats2half2_rn(z[2], z[3]);

@@ -19,6 +19,13 @@ constexpr int KV_MAX_D = 128;
 // one with 99.9% of the weight and no value, a fifth of the output.)
 constexpr float ATTN_HEAD = 7.0f, ATTN_SLACK = 15.0f;
 
+// A mean of fp16 values on its way to fp16. Rounded weights over the sum of unrounded
+// ones can pass the largest value by 2^-11 of it, and fp16 has nothing above 65504 but
+// Inf. Inf and NaN stay as they are.
+__device__ __forceinline__ float mean_to_f16_range(float x) {
+  return fabsf(x) < 131072.0f ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x;
+}
+
 // One layer's pool. Strides in elements of k / v and in floats of the scales.
 struct KvView {
   const uint8_t *k, *v;

@@ -312,3 +312,54 @@ def test_steps_of_the_score_around_the_slack(call):
         bound = 2.0 ** -11 * np.abs(o) + 2.0 ** -25 + (2.0 ** -11 + 2.0 ** -20) * a + t * 2.0 ** -32 * 4
         assert status.item() == 0, r0
         assert (np.abs(out[:, 0].cpu().double().numpy() - o) <= bound).all(), r0
+
+
+# ------------------------------------------------------------------ values at fp16's largest
+@pytest.mark.parametrize("call", ["decode", "decode_long", "prompt", "prompt_cluster"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_means_of_the_largest_value_stay_finite(call, sign):
+    """Every value is 65504, so every mean is. The weights of 15 keys of 16 are just past the middle of
+    two fp16 numbers and are rounded up while their sum is not: half a step above 65504 without a limit."""
+    t = 700
+    b = Batch(bt, [t], 16, 1, 128)
+    k = np.zeros((1, t, 128))
+    k[0, np.arange(t) % 16 != 0, 0] = -1.0                    # one of 16 keys holds the maximum: every share sees it
+    put(b, 0, k, np.full((1, t, 128), sign * 65504.0))
+    scale = -math.log(0.5 + 1.1 * 2.0 ** -12)
+    n = 150 if call == "prompt" else 1
+    q = one_hot_queries(n, 2, 128, {0: 1.0})
+    qt = torch.from_numpy(q).cuda()
+    table = b.table if call in ("decode", "prompt_cluster") else long_rows(b)
+    slots = b.slots.repeat(n)
+    status = bt.new_status()
+    if call.startswith("decode"):
+        out = bt.bwta_attn_decode_paged(qt, b.cache, table, scale, slots=slots, status=status)
+    else:
+        out = bt.bwta_attn_prompt_paged(qt, cu(list(range(n + 1))), b.cache, table, scale, slots=slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and (out == sign * 65504.0).all()
+
+
+@pytest.mark.parametrize("call", ["decode", "decode_long", "prompt", "prompt_cluster"])
+def test_infinite_values_stay_infinite(call):
+    """A value of Inf that every row sees: that column of the output is Inf, the others are what they were."""
+    t, n = 700, 150 if call == "prompt" else 1
+    b = Batch(bt, [t], 16, 1, 64)
+    for j, d, x in ((3, 5, math.inf), (77, 8, -math.inf)):
+        page, at = place(b, 0, j)
+        b.cache.v[page, 0, at, d] = x
+    q = b.queries(n, 2)
+    qt = torch.from_numpy(q).cuda()
+    table = b.table if call in ("decode", "prompt_cluster") else long_rows(b)
+    slots = b.slots.repeat(n)
+    status = bt.new_status()
+    if call.startswith("decode"):
+        out = bt.bwta_attn_decode_paged(qt, b.cache, table, 0.125, slots=slots, status=status)
+    else:
+        out = bt.bwta_attn_prompt_paged(qt, cu(list(range(n + 1))), b.cache, table, 0.125, slots=slots, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == bt.STATUS_NONFINITE
+    assert (out[:, :, 5] == math.inf).all() and (out[:, :, 8] == -math.inf).all()
+    out[:, :, [5, 8]] = 0.0
+    b.v[0][:, :, [5, 8]] = 0.0
+    check_tight(b, q, out, [0] * n, [t - 1] * n, 0.125, rows=8)
