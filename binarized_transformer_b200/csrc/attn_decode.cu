@@ -86,6 +86,12 @@ struct DecArgs {
   int cluster; // blocks of an item (CLUSTER)
 };
 
+// Workspace: the pieces (two of a block), then k_attn_decode's prefix sums for the join.
+__host__ __device__ constexpr int64_t dec_pieces(int rows, int DP) {
+  return (int64_t)DEC_MAX_BLOCKS * 2 * rows * (DP + 2);  // floats; a multiple of 2
+}
+constexpr int DEC_PREFIX = DEC_THREADS + 1;  // 64-bit numbers
+
 // A sequence's tiles with a visible key: [0, sink_tiles) and [first, tiles).
 struct DecSeq {
   int32_t slot, len, sink_tiles, first;
@@ -109,10 +115,11 @@ __device__ __forceinline__ DecSeq dec_seq(const AttnArgs &a, int64_t s) {
   return q;
 }
 
-// Units before each thread's share of the sequences (a share is `per` sequences),
-// for blocks of T threads; before[T] = all of them.
-template <int T, int TILE>
+// Units before each thread's share of the sequences (a share is `per` sequences);
+// before[T] = all of them.
+template <int TILE>
 __device__ __forceinline__ int dec_scan(const AttnArgs &a, int64_t *before, int64_t *sums) {
+  constexpr int T = DEC_THREADS;
   const int per = (int)ceil_div<int64_t>(a.n_seq, T);
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
     for (int i = threadIdx.x * 16; i < S::RING; i += DEC_THREADS * 16)
       *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0, 0, 0, 0);
   pdl_wait();
-  pdl_trigger();  // after the wait: k_attn_join may then read the lengths before its own
+  pdl_trigger();
   DecCursor<TILE> at;
   int n = 0;
   if (CLUSTER) {
@@ -267,8 +274,12 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
     at.unit = (int)div_pos((int64_t)at.q.units * rank, A.cluster);
     n = (int)div_pos((int64_t)at.q.units * (rank + 1), A.cluster) - at.unit;
   } else {
-    const int per = dec_scan<DEC_THREADS, TILE>(a, before, sums);
+    const int per = dec_scan<TILE>(a, before, sums);
     const DecCut cut(before[DEC_THREADS] * items, A.blocks);
+    if (blockIdx.x == 0) {  // what the join needs to find an item's pieces
+      int64_t *prefix = reinterpret_cast<int64_t *>(A.ws + dec_pieces(A.rows, DP));
+      for (int i = threadIdx.x; i < DEC_PREFIX; i += DEC_THREADS) prefix[i] = before[i];
+    }
     if ((int)blockIdx.x >= cut.blocks) return;
     const int64_t u0 = cut.start(blockIdx.x);
     n = (int)(cut.start(blockIdx.x + 1) - u0);
@@ -742,10 +753,11 @@ __global__ void __launch_bounds__(DEC_THREADS, DecShape<DP, E4M3, NB>::BLOCKS) k
 
 // The outputs of items that several blocks share, and of empty sequences: a warp a
 // query head, 4 columns a lane. WIDE, for calls of few items, each spread over many
-// blocks: a block a query head, its warps take the pieces in turn.
+// blocks: a block a query head, its warps take the pieces in turn. Where an item's units
+// lie comes from k_attn_decode's prefix sums (scanning the lengths in every block would
+// be work of n_seq^2).
 template <int DP, int TILE, bool WIDE>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
-  __shared__ int64_t before[JOIN_THREADS + 1], sums[JOIN_THREADS / 32];
   __shared__ float part[WIDE ? JOIN_HEADS : 1][DP + 2];
   const AttnArgs &a = A.a;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -753,25 +765,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
   const int64_t s = blockIdx.x / hb;
   const int hx = (int)(blockIdx.x - s * hb), h = WIDE ? hx : hx * JOIN_HEADS + warp;
   const int D = a.c.D, heads = a.n_heads / a.c.H, items = a.c.H * A.groups;
-  // the table is as k_attn_decode found it; its pieces are what has to be waited for
-  const int per = dec_scan<JOIN_THREADS, TILE>(a, before, sums);
-  const DecSeq q = dec_seq<TILE>(a, s);
-  const DecCut cut(before[JOIN_THREADS] * items, A.blocks);
-  int64_t u = 0;
-  int first = 0, last = 0, row = 0;
-  if (h < a.n_heads && q.units > 0) {
-    const int who = (int)div_pos(s, per), kh = h / heads, hg = (h - kh * heads) / A.per_item;
-    u = before[who] * items;
-    for (int64_t i = (int64_t)who * per; i < s; ++i) u += (int64_t)dec_seq<TILE>(a, i).units * items;
-    u += (int64_t)(kh * A.groups + hg) * q.units;
-    first = cut.owner(u);
-    last = cut.owner(u + q.units - 1);
-    row = h - kh * heads - hg * A.per_item;
-  }
+  const int64_t *prefix = reinterpret_cast<const int64_t *>(A.ws + dec_pieces(A.rows, DP));
+  const int per = (int)ceil_div<int64_t>(a.n_seq, DEC_THREADS), who = (int)div_pos(s, per);
+  const int kh = h / heads, hg = (h - kh * heads) / A.per_item, row = h - kh * heads - hg * A.per_item;
   // No early trigger: blocks of the next kernel that wait here already would take the
   // places of this one's (64 ragged sequences, call after call: 237 us for 211).
   pdl_wait();
   if (h >= a.n_heads) return;
+  int64_t u = prefix[who];
+  const int64_t total = prefix[DEC_THREADS];
+  const DecSeq q = dec_seq<TILE>(a, s);
+  if (per > 1) {  // the sequences between the share's first and this one
+    int64_t x = 0;
+    for (int64_t i = (int64_t)who * per + lane; i < s; i += 32) x += dec_seq<TILE>(a, i).units;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(FULL, x, d);
+    u += x;
+  }
   uint16_t *out = a.out + s * a.ldo + (int64_t)h * D + lane * 4;
   if (q.units == 0) {
     if (WIDE && warp > 0) return;
@@ -779,6 +789,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
     if (lane * 4 < D) *reinterpret_cast<uint2 *>(out) = make_uint2(0, 0);
     return;
   }
+  const DecCut cut(total * items, A.blocks);
+  u = u * items + (int64_t)(kh * A.groups + hg) * q.units;
+  const int first = cut.owner(u), last = cut.owner(u + q.units - 1);
   if (first == last) return;  // written by that block
   // a piece is its block's second one where the item begins: in the first block
   auto piece = [&](int c) {
@@ -856,7 +869,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const DecArgs A) {
 
 int64_t attn_decode_ws(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
   const int64_t rows = std::min<int64_t>(n_heads / std::max<int64_t>(n_kv_heads, 1), DEC_MAX_ROWS);
-  return (int64_t)DEC_MAX_BLOCKS * 2 * rows * ((head_dim <= 64 ? 64 : 128) + 2) * 4;
+  return dec_pieces((int)rows, head_dim <= 64 ? 64 : 128) * 4 + DEC_PREFIX * 8;
 }
 
 template <int DP, bool E4M3, int NB>

@@ -363,3 +363,69 @@ def test_infinite_values_stay_infinite(call):
     out[:, :, [5, 8]] = 0.0
     b.v[0][:, :, [5, 8]] = 0.0
     check_tight(b, q, out, [0] * n, [t - 1] * n, 0.125, rows=8)
+
+
+# ------------------------------------------------------------------ lengths that grow from launch to launch
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("captured", [False, True])
+def test_joined_pieces_follow_the_lengths(e4m3, captured):
+    """reserve, append, decode over and over with nothing between them, in a table whose rows are too long for
+    clusters: every step is cut by lengths that the step before it in the stream has just written."""
+    H, G, D, ps, steps = 2, 4, 64, 16, 24
+    lens, grow = [2990, 100, 63, 1], [1, 1, 1, 1]
+    b = Batch(bt, lens, ps, H, D, e4m3, seed=8)
+    pool = b.num_pages + 40
+    kind = torch.uint8 if e4m3 else torch.float16
+    cache = bt.KvCache.empty(pool, ps, H, D, e4m3=e4m3)
+    for x, y in ((cache.k, b.cache.k), (cache.v, b.cache.v), (cache.k_scale, b.cache.k_scale), (cache.v_scale, b.cache.v_scale)):
+        if x is not None:
+            x[:b.num_pages] = y
+    assert cache.k.dtype == kind
+    ref = torch.zeros(pool, dtype=torch.int32, device="cuda")
+    held = b.table.pages[b.table.pages >= 0].long()
+    ref[held] = 1
+    b.table.refcount = ref
+    table = long_rows(b, 1 << 15)
+    r = np.random.default_rng(41)
+    ks, vs, qs = (r.standard_normal((steps, 4, heads, D)) for heads in (H, H, H * G))
+    ks, vs = (torch.from_numpy(x.astype(np.float32)).cuda() for x in (ks, vs))
+    qs = torch.from_numpy(qs.astype(np.float16)).cuda()
+    k, v, q = ks[0].clone(), vs[0].clone(), qs[0].clone()
+    status, new, ws = bt.new_status(), cu(grow), bt.decode_workspace(H * G, cache)
+
+    def step():
+        bt.bwta_kv_reserve(table, ps, b.slots, new, status=status)
+        bt.bwta_kv_append(cache, table, k, v, slots=b.slots, status=status)
+        return bt.bwta_attn_decode_paged(q, cache, table, 0.125, slots=b.slots, workspace=ws, status=status)
+
+    bt.bwta_attn_decode_paged(q, cache, table, 0.125, slots=b.slots, workspace=ws)  # once outside of the capture
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+    got = []
+    for i in range(steps):
+        k.copy_(ks[i])
+        v.copy_(vs[i])
+        q.copy_(qs[i])
+        if captured:
+            graph.replay()
+        else:
+            out = step()
+        got.append(out.clone())
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for i in range(steps):
+        for s in range(4):
+            for x, keep in ((ks, b.k), (vs, b.v)):
+                row = x[i, s].cpu().double().numpy()[:, None]
+                if e4m3:
+                    codes, sc = quantize_many(row)
+                    row = E4M3[codes] * sc[..., None]
+                else:
+                    row = row.astype(np.float16).astype(np.float64)
+                keep[s] = np.concatenate([keep[s], row], 1)
+        check_tight(b, qs[i].cpu().numpy(), got[i], [0, 1, 2, 3], [n + i for n in lens], 0.125)
+    if captured:
+        graph.reset()
