@@ -29,7 +29,7 @@ LIB_SOURCES = ["pack.cu", "gemm.cu", "decode.cu", "gemm_tc.cu", "attn.cu", "bill
                "kv_append.cu", "kv_pages.cu", "attn_prompt.cu", "attn_decode.cu",
                "kv_abi.cu", "abi.cu"]
 MB_SOURCES = ["microbench.cu"]
-HEADERS = ["common.cuh", "tma.cuh", "quant.cuh", "tcgen05.cuh", "kv.cuh"]
+HEADERS = ["common.cuh", "tma.cuh", "quant.cuh", "tcgen05.cuh", "kv.cuh", "smem_opt_in.h"]
 
 
 def _mtime(p):
