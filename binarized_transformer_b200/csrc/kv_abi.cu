@@ -322,19 +322,30 @@ int bwta_kv_copy_pages(const bwta_kv_cache *src, const bwta_kv_cache *dst, int64
   if (n > BWTA_KV_MAX_POOL) return BWTA_ERR_UNSUPPORTED;
   if (int r = check_workspace(workspace, workspace_bytes, bwta_kv_pages_workspace(0, n))) return r;
   if (n == 0) return BWTA_OK;
-  // one pool (the list then must not read what it writes), or two that share nothing
-  bool same = true, cross = false;
-  for (int64_t i = 0; i < n_layers; ++i) {
-    same = same && src[i].k == dst[i].k && src[i].v == dst[i].v;
-    for (int64_t j = 0; j < n_layers; ++j)
-      cross = cross || src[i].k == dst[j].v || src[i].v == dst[j].k ||
-              (i != j && (src[i].k == dst[j].k || src[i].v == dst[j].v)) ||
-              (i == j && (src[i].k == dst[i].k) != (src[i].v == dst[i].v));
+  // One pool in every layer (the list then must not read what it writes), or two that share
+  // nothing.
+  bool same = true;
+  {
+    bool shared = false;
+    const bool scales = src->type == BWTA_KV_E4M3;
+    for (int64_t i = 0; i < n_layers; ++i) {
+      same = same && src[i].k == dst[i].k && src[i].v == dst[i].v &&
+             (!scales || (src[i].k_scale == dst[i].k_scale && src[i].v_scale == dst[i].v_scale));
+      for (int64_t j = 0; j < n_layers; ++j) {
+        const bool kk = src[i].k == dst[j].k, vv = src[i].v == dst[j].v;
+        const bool ks = scales && src[i].k_scale == dst[j].k_scale, vs = scales && src[i].v_scale == dst[j].v_scale;
+        if (src[i].k == dst[j].v || src[i].v == dst[j].k) return BWTA_ERR_INVALID_ARG;
+        if (scales && (src[i].k_scale == dst[j].v_scale || src[i].v_scale == dst[j].k_scale))
+          return BWTA_ERR_INVALID_ARG;
+        if (i != j && (kk || vv || ks || vs)) return BWTA_ERR_INVALID_ARG;
+        shared = shared || kk || vv || ks || vs;
+      }
+    }
+    if (shared && !same) return BWTA_ERR_INVALID_ARG;
+    if (same && (src->num_pages != dst->num_pages || src->page_stride != dst->page_stride ||
+                 g.src_sc_stride != g.dst_sc_stride))
+      return BWTA_ERR_INVALID_ARG;  // two descriptions of one pool
   }
-  if (cross) return BWTA_ERR_INVALID_ARG;
-  if (same && (src->num_pages != dst->num_pages || src->page_stride != dst->page_stride ||
-               g.src_sc_stride != g.dst_sc_stride))
-    return BWTA_ERR_INVALID_ARG;  // two descriptions of one pool
   return cuda_status(launch_kv_copy(l, g, same, src_pages, dst_pages, n,
                                     static_cast<int32_t *>(workspace), d_status, (cudaStream_t)stream));
 }

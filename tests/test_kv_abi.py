@@ -227,3 +227,28 @@ def test_table_model_keeps_its_books():
             for i in range(m.need(m.len[s])):
                 count[m.pages[s][i]] += 1
         assert count == m.ref
+
+
+def _pools(lib, a, b, n=1):
+    a, b = ((bt.KvCacheC * len(x))(*x) for x in (a, b))
+    return lib.bwta_kv_copy_pages(a, b, len(a), P, P, n, P, 1 << 30, None, None)
+
+
+def test_copies_between_pools_that_coincide_in_some_layers(lib):
+    """One pool in every layer or none: a layer copied within itself would race with the list's other copies."""
+    I = bt.BWTA_ERR_INVALID_ARG
+    A, B, D, E = 0x20000, 0x30000, 0x40000, 0x50000
+    one, two, other = cache(k=A, v=B), cache(k=D, v=E), cache(k=0x60000, v=0x70000)
+    assert _pools(lib, [one, two], [one, other]) == I
+    assert _pools(lib, [two, one], [other, one]) == I
+    assert _pools(lib, [one, two], [cache(k=A, v=B, n=11), cache(k=0x60000, v=0x70000, n=11)]) == I
+
+    def e4m3(k, v, ks, vs):
+        return cache(type=1, k=k, v=v, ks=ks, vs=vs, ss=32)
+    x = e4m3(A, B, 0x1000, 0x2000)
+    assert _pools(lib, [x], [e4m3(D, E, 0x1000, 0x3000)]) == I      # scales shared, bytes not
+    assert _pools(lib, [x], [e4m3(D, E, 0x3000, 0x2000)]) == I
+    assert _pools(lib, [x], [e4m3(D, E, 0x2000, 0x1000)]) == I
+    assert _pools(lib, [x], [e4m3(A, B, 0x1000, 0x3000)]) == I      # bytes shared, scales not
+    y = e4m3(D, E, 0x3000, 0x4000)
+    assert _pools(lib, [x, y], [e4m3(0x60000, 0x70000, 0x3000, 0x6000), e4m3(0x80000, 0x90000, 0x7000, 0x8000)]) == I
