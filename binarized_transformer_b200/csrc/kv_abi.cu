@@ -323,9 +323,10 @@ int bwta_kv_copy_pages(const bwta_kv_cache *src, const bwta_kv_cache *dst, int64
   if (int r = check_workspace(workspace, workspace_bytes, bwta_kv_pages_workspace(0, n))) return r;
   if (n == 0) return BWTA_OK;
   // One pool in every layer (the list then must not read what it writes), or two that share
-  // nothing.
-  bool same = true;
-  {
+  // nothing. Where a pool is empty no copy is made, and its pointers mean nothing.
+  bool same = false;
+  if (src->num_pages > 0 && dst->num_pages > 0) {
+    same = true;
     bool shared = false;
     const bool scales = src->type == BWTA_KV_E4M3;
     for (int64_t i = 0; i < n_layers; ++i) {

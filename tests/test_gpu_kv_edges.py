@@ -429,3 +429,20 @@ def test_joined_pieces_follow_the_lengths(e4m3, captured):
         check_tight(b, qs[i].cpu().numpy(), got[i], [0, 1, 2, 3], [n + i for n in lens], 0.125)
     if captured:
         graph.reset()
+
+
+# ------------------------------------------------------------------ pools without pages
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_copies_where_a_pool_is_empty(e4m3):
+    """No page can be named: each copy is refused on the device, the call is not (empty pools have no buffers,
+    and that both sides' are NULL says nothing)."""
+    void = [bt.KvCache.empty(0, 16, 2, 64, e4m3=e4m3) for _ in range(4)]
+    some = [bt.KvCache.empty(3, 16, 2, 64, e4m3=e4m3) for _ in range(2)]
+    for c in some:
+        c.k.zero_()
+    for a, b in ((void[:1], void[1:2]), (void[:2], void[2:]), (void[:2], some), (some, void[:2]), (void[:2], void[:2])):
+        status = bt.new_status()
+        bt.bwta_kv_copy_pages(a, b, cu([0, 1]), cu([1, 2]), status=status)
+        torch.cuda.synchronize()
+        assert status.item() == kv_common.BAD
+    assert all((c.k == 0).all() for c in some)
