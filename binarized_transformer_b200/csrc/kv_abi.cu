@@ -339,6 +339,13 @@ int bwta_kv_copy_pages(const bwta_kv_cache *src, const bwta_kv_cache *dst, int64
         if (scales && (src[i].k_scale == dst[j].v_scale || src[i].v_scale == dst[j].k_scale))
           return BWTA_ERR_INVALID_ARG;
         if (i != j && (kk || vv || ks || vs)) return BWTA_ERR_INVALID_ARG;
+        // two layers into one target: its pages would hold parts of each
+        if (i < j && ((dst[i].k == dst[j].k && src[i].k != src[j].k) || (dst[i].v == dst[j].v && src[i].v != src[j].v)))
+          return BWTA_ERR_INVALID_ARG;
+        if (scales && i < j &&
+            ((dst[i].k_scale == dst[j].k_scale && src[i].k_scale != src[j].k_scale) ||
+             (dst[i].v_scale == dst[j].v_scale && src[i].v_scale != src[j].v_scale)))
+          return BWTA_ERR_INVALID_ARG;
         shared = shared || kk || vv || ks || vs;
       }
     }

@@ -503,7 +503,8 @@ int bwta_kv_free(const bwta_kv_table *table, int64_t num_pages, int64_t page_siz
  * fork that finds no free page is not made (dst stays empty; NO_PAGE), nor is
  * any later one that needs a page. Refused as BAD_PAGE, without effect: slots
  * out of range, dst not empty or listed before, src with a length past its row.
- * An entry of src's row outside the pool is passed on as it is (BAD_PAGE).
+ * An entry of src's row outside the pool is passed on as it is, or, for a last
+ * page that is not full, leaves dst a page whose contents are as they were (BAD_PAGE).
  *  caches     host array of n_layers layers of one geometry (<= BWTA_KV_MAX_LAYERS)
  *  src, dst   device int32 [n], n <= BWTA_KV_MAX_LIST
  *  workspace  device, 16-byte aligned, bwta_kv_pages_workspace(num_pages, n) bytes;
@@ -522,7 +523,8 @@ int bwta_kv_compact(const bwta_kv_cache *caches, int64_t n_layers, const bwta_kv
 
 /* Copy page src_pages[i] of every layer of src to page dst_pages[i] of dst (the
  * same geometry, but for num_pages and strides; src and dst are the same pool,
- * described alike, or share no memory). The copies happen at once: refused as
+ * described alike, in every layer, or share no memory; the layers of dst share
+ * none with one another). The copies happen at once: refused as
  * BAD_PAGE, without effect, are pages out of range, every copy to a page that the
  * list writes more than once, and, within one pool, every copy from a page that
  * the list writes (other than onto itself).

@@ -252,3 +252,14 @@ def test_copies_between_pools_that_coincide_in_some_layers(lib):
     assert _pools(lib, [x], [e4m3(A, B, 0x1000, 0x3000)]) == I      # bytes shared, scales not
     y = e4m3(D, E, 0x3000, 0x4000)
     assert _pools(lib, [x, y], [e4m3(0x60000, 0x70000, 0x3000, 0x6000), e4m3(0x80000, 0x90000, 0x7000, 0x8000)]) == I
+
+
+def test_copies_of_two_layers_into_one(lib):
+    """A target that is listed for two sources would hold parts of each."""
+    I = bt.BWTA_ERR_INVALID_ARG
+    one, two = cache(k=0x20000, v=0x30000), cache(k=0x40000, v=0x50000)
+    assert _pools(lib, [one, two], [cache(k=0x60000, v=0x70000)] * 2) == I
+    assert _pools(lib, [one, two], [cache(k=0x60000, v=0x70000), cache(k=0x60000, v=0x80000)]) == I
+    a, b = (cache(type=1, k=0x20000 * i, v=0x30000 * i, ks=0x100 * i, vs=0x200 * i, ss=32) for i in (1, 5))
+    to = [cache(type=1, k=0x500000 * i, v=0x700000 * i, ks=0x1000, vs=0x2000 * i, ss=32) for i in (1, 3)]
+    assert _pools(lib, [a, b], to) == I
