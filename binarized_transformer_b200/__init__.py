@@ -474,7 +474,7 @@ class KvCache:
     (E4M3 bytes) with fp32 scales [num_pages, n_kv_heads, page_size]. Pages may be further apart than
     dense (a view of a larger buffer), the inner dimensions are dense. Keeps the tensors alive; their
     storage must stay where it is."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "ref", "device", "n_kv_heads", "head_dim")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c", "ref", "device", "n_kv_heads", "head_dim", "page_size")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         e4m3 = k.dtype == torch.uint8
@@ -502,7 +502,7 @@ class KvCache:
             ls = stride(k_scale, rows)
             assert stride(v_scale, rows) == ls
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.n_kv_heads, self.head_dim = k.device, H, D
+        self.device, self.n_kv_heads, self.head_dim, self.page_size = k.device, H, D, ps
         self.c = KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                           v_scale.data_ptr() if e4m3 else None, P, ps, H, D, ld, ls,
                           KV_E4M3 if e4m3 else KV_F16)
@@ -521,10 +521,11 @@ class KvCache:
 
 class KvTable:
     """Which pages hold which sequence: pages int32 [n_slots, max_pages], kv_len int32 [n_slots],
-    refcount int32 [num_pages] (needed by the page calls only). Keeps the tensors alive."""
-    __slots__ = ("pages", "kv_len", "refcount", "c", "ref", "device")
+    refcount int32 [num_pages] (needed by the page calls only). Keeps the tensors alive. The lengths mean
+    pages of one size: with page_size given, every call on this table refuses another."""
+    __slots__ = ("pages", "kv_len", "refcount", "c", "ref", "device", "page_size")
 
-    def __init__(self, pages, kv_len, refcount=None):
+    def __init__(self, pages, kv_len, refcount=None, page_size=None):
         assert pages.is_cuda and pages.dtype == torch.int32 and pages.dim() == 2
         assert pages.shape[1] <= 1 or pages.stride(1) == 1
         assert kv_len.dtype == torch.int32 and kv_len.shape == pages.shape[:1]
@@ -533,6 +534,7 @@ class KvTable:
             assert refcount.dtype == torch.int32 and refcount.dim() == 1
             assert refcount.is_contiguous() and refcount.device == pages.device
         self.pages, self.kv_len, self.refcount, self.device = pages, kv_len, refcount, pages.device
+        self.page_size = page_size
         n, m = pages.shape
         self.c = KvTableC(pages.data_ptr(), max(pages.stride(0), m) if n > 1 else m, m, n,
                           kv_len.data_ptr(), refcount.data_ptr() if refcount is not None else None)
@@ -540,11 +542,15 @@ class KvTable:
         self.ref = C.byref(self.c)
 
     @staticmethod
-    def empty(n_slots: int, max_pages: int, num_pages: int, device="cuda"):
+    def empty(n_slots: int, max_pages: int, num_pages: int, device="cuda", page_size=None):
         """A table without sequences over a pool of free pages."""
         return KvTable(torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device),
                        torch.zeros(n_slots, dtype=torch.int32, device=device),
-                       torch.zeros(num_pages, dtype=torch.int32, device=device))
+                       torch.zeros(num_pages, dtype=torch.int32, device=device), page_size)
+
+    def counts(self, page_size):
+        """Whether the table's lengths are counted in pages of this size."""
+        return self.page_size is None or self.page_size == page_size
 
 
 class KvLayers:
@@ -627,7 +633,8 @@ def bwta_kv_append(cache: KvCache, table: KvTable, k, v, slots=None, cu_q=None, 
     into the pages. Without cu_q one row for each slot (or for each of `slots`); with it rows
     cu_q[s] .. cu_q[s+1] belong to sequence s and end at its kv_len."""
     dev = cache.device
-    assert table.device == dev and k.dtype == v.dtype and k.dtype in (torch.float16, torch.float32)
+    assert table.device == dev and table.counts(cache.page_size)
+    assert k.dtype == v.dtype and k.dtype in (torch.float16, torch.float32)
     width = cache.n_kv_heads * cache.head_dim
     kp, ldk, n = _kv_rows(k, width, dev)
     vp, ldv, nv = _kv_rows(v, width, dev)
@@ -650,7 +657,8 @@ def bwta_attn_decode_paged(q, cache: KvCache, table: KvTable, softmax_scale: flo
     """Attention of one new token of each sequence over its pages. q fp16 [n_seq, n_heads, head_dim]
     -> out, the same shape. workspace: uint8 of decode_workspace() bytes (allocated when not given)."""
     dev, D = cache.device, cache.head_dim
-    assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
+    assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D
+    assert table.device == dev and table.counts(cache.page_size)
     n, heads = q.shape[0], q.shape[1]
     qp, ldq, _ = _kv_rows(q, heads * D, dev)
     n_seq = _n_seq(table, slots, None, n)
@@ -682,7 +690,8 @@ def bwta_attn_prompt_paged(q, cu_q, cache: KvCache, table: KvTable, softmax_scal
     q fp16 [rows, n_heads, head_dim], rows cu_q[s] .. cu_q[s+1] the newest of sequence s -> out, the
     same shape (rows past the last sequence are left as they are)."""
     dev, D = cache.device, cache.head_dim
-    assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D and table.device == dev
+    assert q.dtype == torch.float16 and q.dim() == 3 and q.shape[2] == D
+    assert table.device == dev and table.counts(cache.page_size)
     n, heads = q.shape[0], q.shape[1]
     qp, ldq, _ = _kv_rows(q, heads * D, dev)
     n_seq = _n_seq(table, slots, cu_q, n)
@@ -701,7 +710,7 @@ def bwta_attn_prompt_paged(q, cu_q, cache: KvCache, table: KvTable, softmax_scal
 def bwta_kv_reserve(table: KvTable, page_size: int, slots, n_new, status=None):
     """Room for n_new[i] more tokens in slot slots[i]; raises kv_len."""
     dev = table.device
-    assert table.refcount is not None and slots.shape == n_new.shape
+    assert table.refcount is not None and slots.shape == n_new.shape and table.counts(page_size)
     _kv_call("bwta_kv_reserve", dev, table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
              _ints(n_new, dev), slots.shape[0], _status(status, dev))
 
@@ -709,7 +718,7 @@ def bwta_kv_reserve(table: KvTable, page_size: int, slots, n_new, status=None):
 def bwta_kv_free(table: KvTable, page_size: int, slots, status=None):
     """Give up the slots' pages."""
     dev = table.device
-    assert table.refcount is not None
+    assert table.refcount is not None and table.counts(page_size)
     _kv_call("bwta_kv_free", dev, table.ref, table.refcount.shape[0], page_size, _ints(slots, dev),
              slots.shape[0], _status(status, dev))
 
@@ -725,7 +734,7 @@ def bwta_kv_fork(caches, table: KvTable, src, dst, workspace=None, status=None):
     l = kv_layers(caches)
     dev = l.device
     assert table.refcount is not None and table.refcount.shape[0] == l.num_pages
-    assert src.shape == dst.shape and table.device == dev
+    assert src.shape == dst.shape and table.device == dev and table.counts(l.page_size)
     ws = pages_workspace(l.num_pages, src.shape[0], dev) if workspace is None else workspace
     assert ws.device == dev and ws.is_contiguous()
     _kv_call("bwta_kv_fork", dev, l.c, l.n, table.ref, _ints(src, dev), _ints(dst, dev), src.shape[0],
@@ -737,7 +746,7 @@ def bwta_kv_compact(caches, table: KvTable, workspace=None, status=None, out=Non
     l = kv_layers(caches)
     dev = l.device
     assert table.refcount is not None and table.refcount.shape[0] == l.num_pages
-    assert table.device == dev
+    assert table.device == dev and table.counts(l.page_size)
     ws = pages_workspace(l.num_pages, 0, dev) if workspace is None else workspace
     assert ws.device == dev and ws.is_contiguous()
     if out is None:

@@ -446,3 +446,29 @@ def test_copies_where_a_pool_is_empty(e4m3):
         torch.cuda.synchronize()
         assert status.item() == kv_common.BAD
     assert all((c.k == 0).all() for c in some)
+
+
+# ------------------------------------------------------------------ a table of one page size
+def test_a_table_refuses_another_page_size():
+    """Pages handed out by one size and read by another would be the wrong ones, without a flag."""
+    table = bt.KvTable.empty(2, 4, 8, page_size=32)
+    small, right = (bt.KvCache.empty(8, ps, 1, 64) for ps in (16, 32))
+    one, slots = cu([1, 1]), cu([0, 1])
+    k = torch.zeros((2, 64), device="cuda")
+    q = torch.zeros((2, 1, 64), dtype=torch.float16, device="cuda")
+
+    def calls(c):
+        ps = c.page_size
+        return [lambda: bt.bwta_kv_reserve(table, ps, slots, one), lambda: bt.bwta_kv_append(c, table, k, k),
+                lambda: bt.bwta_attn_decode_paged(q, c, table, 0.125),
+                lambda: bt.bwta_attn_prompt_paged(q, cu([0, 1, 2]), c, table, 0.125),
+                lambda: bt.bwta_kv_fork(c, table, slots[:1], slots[1:]), lambda: bt.bwta_kv_compact(c, table),
+                lambda: bt.bwta_kv_free(table, ps, slots)]
+    for call in calls(small):
+        with pytest.raises(AssertionError):
+            call()
+    assert (table.kv_len == 0).all()
+    for call in calls(right):
+        call()
+    torch.cuda.synchronize()
+    assert (table.kv_len == 0).all() and (table.refcount == 0).all()
