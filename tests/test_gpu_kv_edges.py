@@ -472,3 +472,26 @@ def test_a_table_refuses_another_page_size():
         call()
     torch.cuda.synchronize()
     assert (table.kv_len == 0).all() and (table.refcount == 0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_sequences_of_unlike_lengths(e4m3):
+    """A thousand sequences, empty ones among them: a share of the cut's prefix sums is several of them, and
+    pieces of a sequence lie in many blocks or one."""
+    r = np.random.default_rng(17)
+    lens = [0, 1, 63, 64, 65, 128, 129, 1000, 5000] + r.integers(0, 700, 15).tolist()
+    b = Batch(bt, lens, 16, 2, 64, e4m3, seed=17)
+    n = 1000
+    who = r.integers(0, len(lens), n)
+    q = b.queries(n, 4)
+    status = bt.new_status()
+    for window, sinks in ((0, 0), (100, 20)):
+        out = bt.bwta_attn_decode_paged(torch.from_numpy(q).cuda(), b.cache, long_rows(b), 0.125, window, sinks,
+                                        slots=b.slots[torch.from_numpy(who).cuda()], status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        empty = np.array([lens[s] == 0 for s in who])
+        assert (out.cpu().numpy()[empty] == 0).all()
+        rows = np.nonzero(~empty)[0]
+        check_tight(b, q[rows], out[torch.from_numpy(rows).cuda()], who[rows], [lens[s] - 1 for s in who[rows]], 0.125,
+                    window, sinks)
