@@ -38,14 +38,21 @@
 // to the scores in fp32; V's, a power of two, to the converted values, which stays
 // exact.
 //
-// Measured on a B200 (a copy moves 6.55 TB/s): fp16, 64 sequences of 0 .. 8191 tokens,
-// 64 query heads on 8 key heads of 128: 1.29 GB in 210 us, 0.94 of the copy's rate;
-// E4M3, 32 sequences, window 4096, 32 heads: 1.10 GB in 200 us, 0.83; a longer cache
-// costs 6.2 TB/s more, 0.94, the rest is the start, the ends of items and the last
-// blocks (about 20 us). The arithmetic is hidden (without the second product the time is
-// the same), the warps are not: two blocks an SM 236 us, 16-token steps 241; E4M3, one
-// sequence of 250,001 tokens: 0.53 GB in 96 us, 0.84. One token over 333 in fp16, in clusters: 10.7 us, the launch and the
-// chain length, page, keys, parts.
+// Measured on a B200 (a copy moves 6.55 TB/s), call after call with inputs that change:
+// fp16, 64 sequences of 0 .. 8191 tokens, 64 query heads on 8 key heads of 128: 1.29 GB in
+// 212 us, 0.93 of the copy's rate; E4M3, 32 sequences, window 4096, 32 heads: 1.10 GB in
+// 214 us, 0.78 (the same inputs again and again: 201 us); E4M3, one sequence of 250,001
+// tokens: 0.53 GB in 101 us, 0.80. A longer cache costs 6.2 TB/s more, 0.94; the rest is
+// the start, the ends of items and the last blocks (about 20 us). The arithmetic is
+// hidden (without the second product the time is the same), the warps are not: two blocks
+// an SM 236 us, 16-token steps 241. One token over 333 in fp16, in clusters: 7.4 us in a
+// row, 10.3 alone: the launch and the chain length, page, keys, parts; in a table with
+// room for 8192 tokens, which takes the other way, 11.2 and 13.4.
+//
+// Widths other than 64 and 128 copy piece by piece with divisions and a test of each row,
+// and multiply over all of DP: bound by the issue slots, not by HBM. The ragged fp16 case
+// at 112, 96, 80 and 40: 229, 212, 199 and 152 us (0.75, 0.70, 0.62, 0.40 of the copy's
+// rate), the windowed E4M3 one 306, 278, 278 and 249 (0.48, 0.46, 0.38, 0.22).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -874,7 +881,7 @@ static cudaError_t launch_decode_t(DecArgs A, cudaStream_t s) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   A.blocks = std::min(std::max(sms, 1) * S::BLOCKS, DEC_MAX_BLOCKS);
   // Clusters where all items run at once and no block can get more than 8 tiles (measured: one
-  // token over 333 12.8 -> 10.7 us; the other way spreads any length over the whole GPU).
+  // token over 333 13.4 -> 10.3 us; the other way spreads any length over the whole GPU).
   const AttnArgs &a = A.a;
   const int64_t items = a.n_seq * a.c.H * A.groups;
   int64_t tiles = ceil_div<int64_t>((int64_t)a.r.max_pages * a.c.ps, S::TILE);

@@ -32,15 +32,16 @@
 // of 0 times a NaN would be one). Every wait is bounded; on a
 // timeout the block flags it, lets its copies and MMAs finish, frees TMEM and returns.
 //
-// Measured on a B200: fp16, 2 x 8192 causal tokens, 32 heads of 128: 1.10 TFLOP in 1.13 ms,
-// 974 TFLOP/s, 0.60 of cuBLAS's burst rate (1.31 ms back to back under the power limit).
+// Measured on a B200, call after call: fp16, 2 x 8192 causal tokens, 32 heads of 128: 1.10
+// TFLOP in 1.30 ms, 847 TFLOP/s, 0.52 of cuBLAS's burst rate and 0.62 of its sustained one
+// (both under the power limit here, SM clock 1.67 GHz; a cool GPU takes 1.13 ms for one).
 // An instruction with N = 64 (the scores of a half) takes as long as one with N = 128, 64
 // cycles at best: 48 of them a step and pair, 3070 cycles of about 3700 that it takes. Whole
 // 128-key scores (32 instructions a step) leave the tensor cores waiting for the softmax
-// and were slower in each form tried: 1.47 ms in one place, 1.67 with the weights beside
-// them, 1.37 with two threads a row and the tiles taking turns. E4M3, a chunk of 2700 rows
-// at 64 heads on 8 key heads, window 4096: 363 GFLOP in 493 us, 735 TFLOP/s; the
-// conversions add to the issue slots (56% taken).
+// and were slower in each form tried (of 1.13 on a cool GPU): 1.47 ms in one place, 1.67
+// with the weights beside them, 1.37 with two threads a row and the tiles taking turns.
+// E4M3, a chunk of 2700 rows at 64 heads on 8 key heads, window 4096: 363 GFLOP in 489 us,
+// 742 TFLOP/s, 0.45 of the burst rate; the conversions add to the issue slots (55% taken).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -917,7 +918,7 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // (As many as the longest walk that the table allows has shares for; measured: 3 rows
-  // over 8000 tokens 129 -> 25 us, while shares of nothing cost 1.4 us.)
+  // over 8000 tokens 129 -> 23 us, while shares of nothing cost 1.4 us.)
   int64_t tiles = ceil_div<int64_t>((int64_t)a.r.max_pages * a.c.ps, PR_T);
   if (a.window)
     tiles = std::min(tiles, (a.window + 2 * A.R) / PR_T + 2 + std::min(tiles, ceil_div<int64_t>(a.sinks, PR_T)));
