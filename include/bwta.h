@@ -467,7 +467,7 @@ int64_t bwta_attn_decode_workspace(int64_t n_heads, int64_t n_kv_heads, int64_t 
  *  q, out   fp16 [total_q][n_heads * head_dim]
  *  Limits: n_heads / n_kv_heads <= 128; scores (softmax_scale * q . k) of at most
  *  2^27 in magnitude (a row whose largest lies past 1.39 * 2^27 becomes NaN, NONFINITE).
- *  In a row that holds an Inf or NaN, outputs of +-65504 are written as Inf too.
+ *  In a row that holds an Inf or NaN, outputs of +-65504 may be written as Inf.
  *  The rest as bwta_attn_decode_paged, but a value that is visible to one row
  *  of a sequence and not finite may reach the sequence's other rows. TIMEOUT
  *  and DRAIN as for the other tensor-core calls. */
