@@ -55,8 +55,8 @@ int main() {
   std::thread small([] { opt(kernel, 20480); });  // while the larger call is under way
   large.join();
   small.join();
-  if (opt(kernel, 30720) != cudaSuccess || attribute < 30720)
-    return std::printf("launched with %d bytes on an attribute of %d\n", 30720, attribute), 1;
+  if (opt(kernel, 32768) != cudaSuccess || attribute < 32768)
+    return std::printf("launched with %d bytes on an attribute of %d\n", 32768, attribute), 1;
   const int before = calls;
   if (opt(kernel, HOLD) != cudaSuccess || calls != before) return std::puts("set again"), 1;
   if (opt(kernel, 2 * HOLD) != cudaSuccess || attribute != 2 * HOLD) return std::puts("not raised"), 1;
